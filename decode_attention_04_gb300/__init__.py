@@ -46,6 +46,8 @@ FD_DEVERR_LEN_NEGATIVE = 1 << 0
 FD_DEVERR_LEN_CLAMPED = 1 << 1
 FD_DEVERR_WAIT_TIMEOUT = 1 << 2
 FD_DEVERR_MIN_LEN = 1 << 3
+FD_DEVERR_PAGE_ID = 1 << 4
+FD_DEVERR_PAGES_EXHAUSTED = 1 << 5
 
 FD_PATH_AUTO = 0
 FD_PATH_SIMT = 1
@@ -59,7 +61,10 @@ EXPORTED = ["fd_plan", "fd_plan_sms", "fd_plan_kv", "fd_plan_sms_kv", "fd_plan_o
             "fd_plan_min_len", "fd_workspace_bytes",
             "fd_decode_attn", "fd_decode_attn_ex", "fd_decode_attn_fp8", "fd_decode_attn_fp8_ex",
             "fd_decode_attn_noalloc", "fd_debug_withhold_copies", "fd_get_device_error", "fd_release",
-            "fd_strerror", "fd_version"]
+            "fd_strerror", "fd_version",
+            "fd_paged_plan", "fd_paged_plan_sms", "fd_paged_attn", "fd_paged_attn_ex", "fd_paged_append",
+            "fd_pages_workspace_bytes", "fd_pages_reserve", "fd_pages_fork", "fd_pages_free", "fd_pages_compact",
+            "fd_pages_copy"]
 
 
 class fd_plan_t(ctypes.Structure):
@@ -92,6 +97,27 @@ class fd_plan_t(ctypes.Structure):
         return "fd_plan_t(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class fd_paged_plan_t(ctypes.Structure):
+    _fields_ = [
+        ("blocks", ctypes.c_int),
+        ("granule", ctypes.c_int),
+        ("min_share", ctypes.c_int),
+        ("num_sms", ctypes.c_int),
+        ("kv_dtype", ctypes.c_int),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("B", ctypes.c_int),
+        ("NH", ctypes.c_int),
+        ("NKV", ctypes.c_int),
+        ("HS", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("max_pages", ctypes.c_int),
+        ("window", ctypes.c_int),
+    ]
+
+    def __repr__(self):
+        return "fd_paged_plan_t(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
 class FdError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -112,7 +138,7 @@ def load_library(path: Path | str | None = None):
                            "(python -m decode_attention_04_gb300.build)")
     lib = ctypes.CDLL(str(p))
     ci, vp, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
-    planp = ctypes.POINTER(fd_plan_t)
+    planp, ppagedp, ll = ctypes.POINTER(fd_plan_t), ctypes.POINTER(fd_paged_plan_t), ctypes.c_longlong
     sig = {
         "fd_plan": (ci, [ci, ci, ci, ci, ci, ci, ci, ci, planp]),
         "fd_plan_sms": (ci, [ci, ci, ci, ci, ci, ci, ci, ci, ci, ci, planp]),
@@ -134,6 +160,17 @@ def load_library(path: Path | str | None = None):
         "fd_release": (None, []),
         "fd_strerror": (ctypes.c_char_p, [ci]),
         "fd_version": (ci, []),
+        "fd_paged_plan": (ci, [ci] * 9 + [ppagedp]),
+        "fd_paged_plan_sms": (ci, [ci] * 9 + [ppagedp]),
+        "fd_paged_attn": (ci, [vp] * 8 + [ci] * 8 + [ctypes.c_float, ci, vp]),
+        "fd_paged_attn_ex": (ci, [ppagedp, vp, sz] + [vp] * 9 + [ci] * 8 + [ctypes.c_float, vp]),
+        "fd_paged_append": (ci, [vp] * 10 + [ci] * 7 + [ll, ll, ci, vp]),
+        "fd_pages_workspace_bytes": (sz, [ci, ci]),
+        "fd_pages_reserve": (ci, [vp] * 7 + [sz] + [ci] * 4 + [vp]),
+        "fd_pages_fork": (ci, [vp] * 6 + [ci] * 4 + [vp]),
+        "fd_pages_free": (ci, [vp] * 4 + [ci] * 5 + [vp]),
+        "fd_pages_compact": (ci, [vp] * 4 + [sz] + [ci] * 3 + [vp]),
+        "fd_pages_copy": (ci, [vp] * 5 + [ci] * 7 + [vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -351,4 +388,123 @@ def decode_attention(q, k_cache, v_cache, lens, window=0, scale=0.0, out=None, s
     return out
 
 
-__all__ = EXPORTED + ["fd_plan_t", "FdError", "load_library", "decode_attention", "LIB_PATH"]
+# ------------------------------------------------------- the cache in pages
+
+
+def fd_paged_plan(B, NH, NKV, HS, page_size, max_pages, window, device=None, kv_dtype=FD_KV_BF16) -> fd_paged_plan_t:
+    if device is None:
+        import torch
+        device = torch.cuda.current_device()
+    p = fd_paged_plan_t()
+    _check(load_library().fd_paged_plan(B, NH, NKV, HS, page_size, max_pages, window, int(device), int(kv_dtype),
+                                        ctypes.byref(p)), "fd_paged_plan")
+    return p
+
+
+def fd_paged_plan_sms(B, NH, NKV, HS, page_size, max_pages, window, num_sms, kv_dtype=FD_KV_BF16) -> fd_paged_plan_t:
+    p = fd_paged_plan_t()
+    _check(load_library().fd_paged_plan_sms(B, NH, NKV, HS, page_size, max_pages, window, int(num_sms), int(kv_dtype),
+                                            ctypes.byref(p)), "fd_paged_plan_sms")
+    return p
+
+
+def fd_paged_attn(q, k_pages, v_pages, k_scale, v_scale, out, table, lens, B, NH, NKV, HS, page_size, num_pages,
+                  max_pages, window, scale, kv_dtype, stream=None) -> None:
+    _check(load_library().fd_paged_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                                        _ptr(out), _ptr(table), _ptr(lens), B, NH, NKV, HS, page_size, num_pages,
+                                        max_pages, window, float(scale), kv_dtype, _stream(stream)), "fd_paged_attn")
+
+
+def fd_paged_attn_ex(plan: fd_paged_plan_t, workspace, workspace_bytes, out_f32, q, k_pages, v_pages, k_scale, v_scale,
+                     out, table, lens, B, NH, NKV, HS, page_size, num_pages, max_pages, window, scale,
+                     stream=None) -> None:
+    _check(load_library().fd_paged_attn_ex(ctypes.byref(plan), _ptr(workspace), int(workspace_bytes), _ptr(out_f32),
+                                           _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                                           _ptr(out), _ptr(table), _ptr(lens), B, NH, NKV, HS, page_size, num_pages,
+                                           max_pages, window, float(scale), _stream(stream)), "fd_paged_attn_ex")
+
+
+def fd_paged_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, table, lens, start, count, B, T, NKV, HS,
+                    page_size, num_pages, max_pages, k_stride, v_stride, kv_dtype, stream=None) -> None:
+    _check(load_library().fd_paged_append(_ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                                          _ptr(v_scale), _ptr(table), _ptr(lens), _ptr(start), _ptr(count), B, T, NKV,
+                                          HS, page_size, num_pages, max_pages, int(k_stride), int(v_stride), kv_dtype,
+                                          _stream(stream)), "fd_paged_append")
+
+
+def fd_pages_workspace_bytes(B, num_pages) -> int:
+    return load_library().fd_pages_workspace_bytes(B, num_pages)
+
+
+def fd_pages_reserve(table, lens, refs, grow, granted, moves, workspace, workspace_bytes, B, max_pages, num_pages,
+                     page_size, stream=None) -> None:
+    _check(load_library().fd_pages_reserve(_ptr(table), _ptr(lens), _ptr(refs), _ptr(grow), _ptr(granted),
+                                           _ptr(moves), _ptr(workspace), int(workspace_bytes), B, max_pages,
+                                           num_pages, page_size, _stream(stream)), "fd_pages_reserve")
+
+
+def fd_pages_fork(table, lens, parent, table_out, lens_out, refs, B, B_out, max_pages, num_pages, stream=None) -> None:
+    _check(load_library().fd_pages_fork(_ptr(table), _ptr(lens), _ptr(parent), _ptr(table_out), _ptr(lens_out),
+                                        _ptr(refs), B, B_out, max_pages, num_pages, _stream(stream)), "fd_pages_fork")
+
+
+def fd_pages_free(table, lens, refs, keep, window, B, max_pages, num_pages, page_size, stream=None) -> None:
+    _check(load_library().fd_pages_free(_ptr(table), _ptr(lens), _ptr(refs), _ptr(keep), window, B, max_pages,
+                                        num_pages, page_size, _stream(stream)), "fd_pages_free")
+
+
+def fd_pages_compact(table, refs, moves, workspace, workspace_bytes, B, max_pages, num_pages, stream=None) -> None:
+    _check(load_library().fd_pages_compact(_ptr(table), _ptr(refs), _ptr(moves), _ptr(workspace),
+                                           int(workspace_bytes), B, max_pages, num_pages, _stream(stream)),
+           "fd_pages_compact")
+
+
+def fd_pages_copy(k_pages, v_pages, k_scale, v_scale, moves, room, layers, num_pages, NKV, page_size, HS, kv_dtype,
+                  stream=None) -> None:
+    _check(load_library().fd_pages_copy(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(moves), room,
+                                        layers, num_pages, NKV, page_size, HS, kv_dtype, _stream(stream)),
+           "fd_pages_copy")
+
+
+def paged_attention(q, k_pages, v_pages, table, lens, window=0, scale=0.0, k_scale=None, v_scale=None, out=None,
+                    stream=None):
+    """Convenience form over torch tensors: q [B,NH,HS] bf16, pages
+    [num_pages,NKV,page_size,HS] (bf16, or E4M3 codes with k_scale and v_scale
+    [num_pages,NKV] fp32), table int32 [B,max_pages], lens int32 [B], all
+    contiguous on the current device. Allocates `out` if not given and calls
+    fd_paged_attn."""
+    import torch
+    B, NH, HS = q.shape
+    num_pages, NKV, page_size, _ = k_pages.shape
+    if out is None:
+        out = torch.empty_like(q)
+    kv_dtype = FD_KV_BF16 if k_scale is None else FD_KV_E4M3
+    _require(q=(q, torch.bfloat16, (B, NH, HS)), out=(out, torch.bfloat16, (B, NH, HS)),
+             k_pages=(k_pages, _code_types() if kv_dtype else torch.bfloat16, (num_pages, NKV, page_size, HS)),
+             v_pages=(v_pages, _code_types() if kv_dtype else torch.bfloat16, (num_pages, NKV, page_size, HS)),
+             table=(table, torch.int32, (B, table.shape[-1])), lens=(lens, torch.int32, (B,)))
+    if kv_dtype:
+        _require(k_scale=(k_scale, torch.float32, (num_pages, NKV)), v_scale=(v_scale, torch.float32, (num_pages, NKV)))
+    fd_paged_attn(q, k_pages, v_pages, k_scale, v_scale, out, table, lens, B, NH, NKV, HS, page_size, num_pages,
+                  table.shape[1], window, scale, kv_dtype, stream)
+    return out
+
+
+def _code_types():
+    import torch
+    return (torch.uint8, torch.float8_e4m3fn)
+
+
+def _require(**tensors):
+    """The convenience forms hand bare addresses on: a tensor of another type,
+    shape, layout or device is refused here."""
+    import torch
+    for name, (t, dtype, shape) in tensors.items():
+        ok = (t is not None and t.is_cuda and t.device.index == torch.cuda.current_device() and t.is_contiguous() and
+              tuple(t.shape) == tuple(shape))
+        if not ok or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+            raise FdError(FD_ERR_INVALID_ARG, f"{name}: contiguous tensor {tuple(shape)} of {dtype} on the current CUDA device expected")
+
+
+__all__ = EXPORTED + ["fd_plan_t", "fd_paged_plan_t", "FdError", "load_library", "decode_attention", "paged_attention",
+                      "LIB_PATH"]

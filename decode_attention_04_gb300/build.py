@@ -24,7 +24,8 @@ BUILD_DIR = PKG / "_build"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", str(INCLUDE), "-I", str(CSRC)] + ARCH
-SOURCES = ["fd_kernels.cu", "fd_umma.cu", "fd_api.cpp", "fd_noalloc.cu"]
+SOURCES = ["fd_kernels.cu", "fd_umma.cu", "fd_api.cpp", "fd_noalloc.cu",
+           "fd_paged_attn.cu", "fd_pages.cu", "fd_paged_api.cpp"]
 
 
 def nvcc() -> str:

@@ -17,6 +17,7 @@
 
 #include "fd_decode_attn.h"
 #include "fd_internal.h"
+#include "fd_paged.h"
 
 namespace {
 
@@ -622,20 +623,25 @@ int fd_decode_attn_fp8(const void* q, const void* k8, const void* v8, const floa
 int fd_debug_withhold_copies(int withhold_tile, unsigned long long wait_limit_ns) {
   const bool on = withhold_tile >= 0;
   const unsigned long long ns = on ? wait_limit_ns : 0;
-  if (fd::set_wait_limit(ns) != cudaSuccess || fd::set_wait_limit_umma(ns) != cudaSuccess) return FD_ERR_CUDA;
+  if (fd::set_wait_limit(ns) != cudaSuccess || fd::set_wait_limit_umma(ns) != cudaSuccess ||
+      fd::set_wait_limit_paged(ns) != cudaSuccess)
+    return FD_ERR_CUDA;
   g_withhold_tile.store(on ? withhold_tile : INT_MAX, std::memory_order_relaxed);
   return FD_OK;
 }
 
 int fd_get_device_error(fd_stream_t stream, unsigned int* err) {
   if (!err) return FD_ERR_INVALID_ARG;
-  return fd::read_and_clear_device_error(reinterpret_cast<cudaStream_t>(stream), err) == cudaSuccess
+  return fd::read_and_clear_device_error(reinterpret_cast<cudaStream_t>(stream), err) == cudaSuccess &&
+                 fd::read_and_clear_device_error_paged(err) == cudaSuccess &&
+                 fd::read_and_clear_device_error_pages(err) == cudaSuccess
              ? FD_OK
              : FD_ERR_CUDA;
 }
 
 void fd_release(void) {
   fd::noalloc_forget();
+  fd::paged_release();
   std::lock_guard<std::mutex> lk(g_mu);
   for (auto& kv : g_ws) {
     if (kv.second.ptr) {
@@ -653,7 +659,8 @@ const char* fd_strerror(int status) {
   switch (status) {
     case FD_OK: return "ok";
     case FD_ERR_INVALID_ARG: return "invalid argument";
-    case FD_ERR_UNSUPPORTED: return "unsupported shape (HS must be 64/128/256/512, NH % NKV == 0, NH/NKV <= 16)";
+    case FD_ERR_UNSUPPORTED: return "unsupported shape (HS must be 64/128/256/512, NH % NKV == 0, NH/NKV <= 16, "
+                                    "page_size 16/32/64/128, max_pages * page_size < 2^31)";
     case FD_ERR_ALIGNMENT: return "pointer not aligned (16 bytes for tensors and workspace, 4 for lens)";
     case FD_ERR_CUDA: return "CUDA runtime call or kernel launch failed";
     case FD_ERR_WORKSPACE: return "workspace too small, or would need allocating while the stream is captured";
@@ -663,6 +670,6 @@ const char* fd_strerror(int status) {
   }
 }
 
-int fd_version(void) { return (0 << 16) | (1 << 8) | 0; }
+int fd_version(void) { return (0 << 16) | (2 << 8) | 0; }
 
 }  // extern "C"

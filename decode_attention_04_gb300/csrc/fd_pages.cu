@@ -1,0 +1,550 @@
+// The pages of a cache (fd_paged_attn.h): writing new tokens into them, and their
+// bookkeeping - growing, forking, freeing, compacting, copying.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <algorithm>
+#include <cstdint>
+
+#include "fd_decode_attn.h"
+#include "fd_internal.h"
+#include "fd_paged.h"
+#include "fd_paged_attn.h"
+
+namespace fd {
+namespace {
+
+#include "fd_device.cuh"
+
+// ================================================================== appending
+
+// Tokens of one sequence that fall into one page.
+struct Segment {
+  int b;        // sequence
+  int row;      // first row of k_new / v_new
+  int n;        // tokens
+  int slot;     // first slot that is written
+  int page;     // page id; -1: leave the tokens out
+};
+
+// Segment number `seg` of sequence b; n = 0 where there is none. The sequence's
+// new tokens are rows [r0, r0 + n) at positions [lens[b] - n, lens[b]); with
+// `count` the rows behind the first count[b] are left out, and lens[b] counts
+// what was granted. Rows outside [0, T) and negative positions are left out.
+__device__ __forceinline__ Segment segment_of(const AppendArgs& a, int b, int seg, bool report) {
+  Segment s{b, 0, 0, 0, -1};
+  long long r0 = b, n = 1;
+  if (a.start) {
+    r0 = a.start[b];
+    n = a.start[b + 1] - r0;
+  }
+  if (a.count) n = min(n, static_cast<long long>(max(a.count[b], 0)));
+  if (n <= 0) return s;
+  if (report && seg == 0 && (r0 < 0 || r0 + n > a.T)) atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+  const long long at = static_cast<long long>(a.lens[b]) - n;  // position of row r0
+  const long long i0 = max(max(0ll, -r0), -at), i1 = min(n, a.T - r0);
+  if (i0 >= i1) return s;
+  const long long first = at + i0, end = at + i1;
+  const long long j = first / a.P + seg;  // column of the table
+  const long long p0 = max(first, j * a.P), p1 = min(end, (j + 1) * a.P);
+  if (p0 >= p1) return s;
+  if (j >= a.max_pages) {
+    if (report) atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+    return s;
+  }
+  s.row = static_cast<int>(r0 + (p0 - at));
+  s.n = static_cast<int>(p1 - p0);
+  s.slot = static_cast<int>(p0 - j * a.P);
+  s.page = a.table[static_cast<size_t>(b) * a.max_pages + j];
+  if (s.page < 0 || s.page >= a.num_pages) {
+    if (report) atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+    s.page = -1;
+    s.n = 0;
+  }
+  return s;
+}
+
+// Units of work. A sequence that writes n tokens touches at most n / P + 2
+// pages, so with first(b) = start[b] / P + 2 b the segments of sequence b have
+// the numbers first(b) .. first(b + 1) - 1 to themselves, and a unit finds its
+// sequence by a search in `start`.
+__device__ __forceinline__ long long first_unit(const AppendArgs& a, int b) {
+  return static_cast<long long>(max(a.start[b], 0) / a.P) + 2ll * b;
+}
+
+__device__ __forceinline__ Segment find_segment(const AppendArgs& a, long long unit, bool report) {
+  if (!a.start) return segment_of(a, static_cast<int>(unit), 0, report);
+  int lo = 0, hi = a.B;  // the last b with first_unit(b) <= unit
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first_unit(a, mid) <= unit) lo = mid;
+    else hi = mid;
+  }
+  const long long seg = unit - first_unit(a, lo);
+  if (seg < 0 || seg > 0x3fffffff) return Segment{lo, 0, 0, 0, -1};
+  return segment_of(a, lo, static_cast<int>(seg), report);
+}
+
+__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
+  return __half2float(__half(h));
+}
+
+// Nearest E4M3 code of x / s: NaN where x is not finite, 0 where s is 0.
+__device__ __forceinline__ uint8_t quantise(float x, float s) {
+  const float y = isfinite(x) ? (s > 0.f ? x / s : 0.f) : __int_as_float(0x7fffffff);
+  return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Least power of two s with amax <= 448 s, at least 2^-126; 0 for amax = 0.
+// 448 = 1.75 * 2^8, so s = 2^(e - 8) where amax = m 2^e with m <= 1.75.
+__device__ __forceinline__ float block_scale(float amax) {
+  if (!(amax > 0.f)) return 0.f;
+  const uint32_t u = __float_as_uint(amax);
+  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
+}
+
+constexpr int kAppendThreads = 128;
+
+// One block per (unit, head, K or V).
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  __shared__ float red[kAppendThreads / 32];
+  const int head = blockIdx.y, w = blockIdx.z, tid = threadIdx.x;
+  const Segment g = find_segment(a, blockIdx.x, head == 0 && w == 0 && tid == 0);
+  if (g.n <= 0) return;
+  const size_t block = static_cast<size_t>(g.page) * a.NKV + head;
+  const size_t base = (block * a.P + g.slot) * a.HS;
+  const int rowv = a.HS / 8;  // vectors of 8 elements in a row
+  const uint16_t* x = a.x[w] + static_cast<long long>(g.row) * a.stride[w] + static_cast<size_t>(head) * a.HS;
+  if (!a.kv8) {
+    uint16_t* to = static_cast<uint16_t*>(a.pages[w]) + base;
+    for (int i = tid; i < g.n * rowv; i += kAppendThreads)
+      reinterpret_cast<uint4*>(to)[i] =
+          *reinterpret_cast<const uint4*>(x + static_cast<long long>(i / rowv) * a.stride[w] + (i % rowv) * 8);
+    return;
+  }
+  float amax = 0.f;
+  for (int i = tid; i < g.n * rowv; i += kAppendThreads) {
+    const uint16_t* at = x + static_cast<long long>(i / rowv) * a.stride[w] + (i % rowv) * 8;
+    for (int k = 0; k < 8; ++k) {
+      const float f = fabsf(bf16_bits_to_f32(at[k]));
+      if (isfinite(f)) amax = fmaxf(amax, f);
+    }
+  }
+  for (int i = 16; i; i >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, i));
+  if ((tid & 31) == 0) red[tid >> 5] = amax;
+  const float old = g.slot > 0 ? a.scale[w][block] : 0.f;
+  __syncthreads();
+  for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, red[i]);
+  const float s = fmaxf(block_scale(amax), old);
+  uint8_t* pages = static_cast<uint8_t*>(a.pages[w]);
+  if (g.slot > 0 && s > old) {
+    const float ratio = old / s;
+    uint8_t* held = pages + block * a.P * a.HS;
+    for (int i = tid; i < g.slot * a.HS; i += kAppendThreads) held[i] = quantise(e4m3_to_f32(held[i]) * ratio, 1.f);
+  }
+  uint8_t* to = pages + base;
+  for (int i = tid; i < g.n * a.HS; i += kAppendThreads)
+    to[i] = quantise(bf16_bits_to_f32(x[static_cast<long long>(i / a.HS) * a.stride[w] + i % a.HS]), s);
+  if (tid == 0) a.scale[w][block] = s;
+}
+
+// ================================================================ bookkeeping
+
+// reserve and compact put the pages in order, which takes prefix sums over all
+// of refs: one cluster of 8 blocks does that in one launch, each block a
+// consecutive range of the pages, the ranges' totals exchanged through
+// distributed shared memory.
+constexpr int kCluster = 8;
+constexpr int kBookThreads = 1024;
+
+__device__ __forceinline__ int page_free(int refs) { return refs <= 0 ? 1 : 0; }
+
+// Exclusive prefix sum over the block; *total gets the sum.
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T* warp_sums, T* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T inc = x;
+  for (int i = 1; i < 32; i <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, inc, i);
+    if (lane >= i) inc += y;
+  }
+  __syncthreads();  // warp_sums may still be read from the scan before
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  T before = 0, all = 0;
+  for (int i = 0; i < kBookThreads / 32; ++i) {
+    const T y = warp_sums[i];
+    if (i < warp) before += y;
+    all += y;
+  }
+  *total = all;
+  return before + inc - x;
+}
+
+__device__ __forceinline__ int ld_dsmem_int(const int* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
+  return static_cast<int>(v);
+}
+
+// This block's range of the pages: consecutive, a multiple of the block's step.
+__device__ __forceinline__ void page_range(int num_pages, int* first, int* last) {
+  const long long step = kBookThreads;
+  const long long per = ((num_pages + kCluster - 1ll) / kCluster + step - 1) / step * step;
+  *first = static_cast<int>(min(per * cluster_ctarank(), static_cast<long long>(num_pages)));
+  *last = static_cast<int>(min(per * (cluster_ctarank() + 1ll), static_cast<long long>(num_pages)));
+}
+
+// Counts the pages of the range for which `want` holds, and gives the number
+// of such pages in the ranges before this one and in all of them.
+template <class F>
+__device__ __forceinline__ void count_pages(int first, int last, int* mine, int* warp_sums, F want, int* before,
+                                            int* all) {
+  int n = 0;
+  for (int p = first + static_cast<int>(threadIdx.x); p < last; p += kBookThreads) n += want(p);
+  int total;
+  block_scan(n, warp_sums, &total);
+  if (threadIdx.x == 0) *mine = total;
+  cluster_sync_all();
+  int b = 0, t = 0;
+  for (int r = 0; r < kCluster; ++r) {
+    const int y = ld_dsmem_int(mine, r);
+    if (r < static_cast<int>(cluster_ctarank())) b += y;
+    t += y;
+  }
+  *before = b;
+  *all = t;
+}
+
+// Workspace of reserve, behind the header: four arrays of B ints.
+//   begin: free pages handed out to the sequences before (clamped)
+//   have:  pages of the row before the call
+//   copy:  number of the move, or -1
+//   from:  the shared page
+// header[0]: pages handed out in all.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
+    reserve_kernel(int* table, int* lens, int* refs, const int* grow, int* granted, int* moves, int* ws, int B,
+                   int max_pages, int num_pages, int P) {
+  __shared__ int mine, warp_sums[kBookThreads / 32];
+  __shared__ long long warp_sums64[kBookThreads / 32];
+  const int tid = threadIdx.x;
+  int *begin = ws + kPagesHeader, *have = begin + B, *copy = have + B, *from = copy + B;
+  int first, last, before, free_all;
+  page_range(num_pages, &first, &last);
+  count_pages(first, last, &mine, warp_sums, [&](int p) { return page_free(refs[p]); }, &before, &free_all);
+  if (cluster_ctarank() == 0) {
+    long long upto = 0;  // pages needed by the sequences before this chunk
+    int taken = 0, copies = 0;
+    for (int b0 = 0; b0 < B; b0 += kBookThreads) {
+      const int b = b0 + tid;
+      int old = 0, n = 0, held = 0, src = -1, shared = 0, fits = 1;
+      long long need = 0;
+      if (b < B) {
+        old = max(lens[b], 0);
+        n = grow ? max(grow[b], 0) : 1;
+        held = old / P + (old % P != 0);
+        const long long want = (static_cast<long long>(old) + n + P - 1) / P;
+        if (n > 0 && (want > max_pages || held > max_pages)) {
+          fits = 0;
+        } else if (n > 0 && old % P != 0) {
+          src = table[static_cast<size_t>(b) * max_pages + old / P];
+          if (src < 0 || src >= num_pages) {
+            atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+            fits = 0;
+          } else {
+            shared = refs[src] > 1;
+          }
+        }
+        if (n > 0 && fits) need = want - held + shared;
+      }
+      long long chunk;
+      const long long at = upto + block_scan(need, warp_sums64, &chunk);
+      const bool given = n > 0 && fits && (need == 0 || at + need <= free_all);
+      int chunk_copies, chunk_taken;
+      const int move = copies + block_scan(given && shared ? 1 : 0, warp_sums, &chunk_copies);
+      block_scan(given ? static_cast<int>(need) : 0, warp_sums, &chunk_taken);
+      if (b < B) {
+        begin[b] = static_cast<int>(min(at, static_cast<long long>(num_pages)));
+        have[b] = held;
+        copy[b] = given && shared ? move : -1;
+        from[b] = src;
+        granted[b] = given ? n : 0;
+        if (given) lens[b] = old + n;
+        else if (n > 0) atomicOr(&g_device_error, FD_DEVERR_PAGES_EXHAUSTED);
+      }
+      upto += chunk;
+      taken += chunk_taken;
+      copies += chunk_copies;
+    }
+    if (tid == 0) {
+      ws[0] = taken;
+      moves[0] = copies;
+      moves[1] = free_all - taken;
+    }
+  }
+  cluster_sync_all();
+  const int taken = __ldcg(ws);
+  // the free page of rank r goes to the last sequence with begin <= r
+  for (int p0 = first; p0 < last && before < taken; p0 += kBookThreads) {
+    const int p = p0 + tid;
+    const int is_free = p < last ? page_free(refs[p]) : 0;
+    int total;
+    const int r = before + block_scan(is_free, warp_sums, &total);
+    if (is_free && r < taken) {
+      int lo = 0, hi = B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldcg(begin + mid) <= r) lo = mid;
+        else hi = mid;
+      }
+      const int j = r - __ldcg(begin + lo), c = __ldcg(copy + lo), h = __ldcg(have + lo);
+      if (c >= 0 && j == 0) {
+        table[static_cast<size_t>(lo) * max_pages + h - 1] = p;
+        moves[2 + 2 * static_cast<size_t>(c)] = __ldcg(from + lo);
+        moves[3 + 2 * static_cast<size_t>(c)] = p;
+      } else {
+        table[static_cast<size_t>(lo) * max_pages + h + j - (c >= 0)] = p;
+      }
+      refs[p] = 1;
+    }
+    before += total;
+  }
+  cluster_sync_all();  // every block has read refs: now the copied pages lose their rows
+  if (cluster_ctarank() == 0)
+    for (int b = tid; b < B; b += kBookThreads)
+      if (copy[b] >= 0) atomicSub(refs + from[b], 1);
+}
+
+// The i-th page in use with a number >= n takes the i-th free number < n, n =
+// pages in use. With r = pages in use before page p: a free page p < n is hole
+// p - r, and a page in use p >= n is mover r - (pages in use below n).
+// ws[r] = p for those movers and ws[p] = r (distinct places, as r < n <= p).
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
+    compact_kernel(int* refs, int* moves, int* ws, int num_pages) {
+  __shared__ int mine, holes, warp_sums[kBookThreads / 32];
+  const int tid = threadIdx.x;
+  int first, last, before, n;
+  page_range(num_pages, &first, &last);
+  count_pages(first, last, &mine, warp_sums, [&](int p) { return 1 - page_free(refs[p]); }, &before, &n);
+  int my_holes = 0;
+  for (int p0 = first; p0 < last; p0 += kBookThreads) {
+    const int p = p0 + tid;
+    const int used = p < last ? 1 - page_free(refs[p]) : 0;
+    int total;
+    const int r = before + block_scan(used, warp_sums, &total);
+    if (p < last && !used && p < n) {
+      moves[3 + 2 * static_cast<size_t>(p - r)] = p;
+      ++my_holes;
+    }
+    if (used && p >= n) {
+      ws[r] = p;
+      ws[p] = r;
+    }
+    before += total;
+  }
+  int total;
+  block_scan(my_holes, warp_sums, &total);
+  if (tid == 0) holes = total;
+  cluster_sync_all();
+  int moved = 0;
+  for (int r = 0; r < kCluster; ++r) moved += ld_dsmem_int(&holes, r);
+  const int below = n - moved;  // pages in use below n
+  for (int i = cluster_ctarank() * kBookThreads + tid; i < moved; i += kCluster * kBookThreads) {
+    const int src = __ldcg(ws + below + i), dst = __ldcg(moves + 3 + 2 * static_cast<size_t>(i));
+    moves[2 + 2 * static_cast<size_t>(i)] = src;
+    refs[dst] = refs[src];
+    refs[src] = 0;
+  }
+  if (cluster_ctarank() == 0 && tid == 0) {
+    moves[0] = moved;
+    moves[1] = num_pages - n;
+  }
+  cluster_sync_all();  // no block leaves while another reads its shared memory
+}
+
+constexpr int kTableThreads = 256;
+
+// Table entries follow the moves of compact_kernel.
+__global__ void __launch_bounds__(kTableThreads)
+    renumber_kernel(int* table, const int* moves, const int* ws, long long entries, int num_pages) {
+  const int n = num_pages - moves[1], below = n - moves[0];
+  for (long long i = blockIdx.x * static_cast<long long>(kTableThreads) + threadIdx.x; i < entries;
+       i += static_cast<long long>(gridDim.x) * kTableThreads) {
+    const int p = table[i];
+    if (p < n) continue;
+    if (p >= num_pages) {
+      atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+      continue;
+    }
+    // a page that refs calls free is no mover: its entry, which broke the
+    // invariant before the call, keeps its number
+    const int k = ws[p] - below;
+    if (k >= 0 && k < moves[0] && moves[2 + 2 * static_cast<size_t>(k)] == p)
+      table[i] = moves[3 + 2 * static_cast<size_t>(k)];
+  }
+}
+
+__global__ void __launch_bounds__(kTableThreads)
+    fork_kernel(const int* table, const int* lens, const int* parent, int* table_out, int* lens_out, int* refs, int B,
+                int B_out, int max_pages, int num_pages) {
+  const int i = blockIdx.y;  // a row: old, new or both
+  int from = -1;
+  if (i < B_out) {
+    from = parent[i];
+    if (from < -1 || from >= B) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+      from = -1;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) lens_out[i] = from >= 0 ? lens[from] : 0;
+  }
+  for (int j = blockIdx.x * kTableThreads + threadIdx.x; j < max_pages; j += gridDim.x * kTableThreads) {
+    int got = -1;
+    if (i < B_out) {
+      if (from >= 0) {
+        got = table[static_cast<size_t>(from) * max_pages + j];
+        if (got < 0) got = -1;
+        if (got >= num_pages) {
+          atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+          got = -1;
+        }
+      }
+      table_out[static_cast<size_t>(i) * max_pages + j] = got;
+    }
+    // a row that is its own parent changes no count
+    if (from == i) continue;
+    if (got >= 0) atomicAdd(refs + got, 1);
+    if (i < B) {
+      const int was = table[static_cast<size_t>(i) * max_pages + j];
+      if (was >= 0 && was < num_pages) atomicSub(refs + was, 1);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kTableThreads)
+    free_kernel(int* table, int* lens, int* refs, const int* keep, int window, int max_pages, int num_pages, int P) {
+  const int b = blockIdx.y;
+  // every thread of the row takes this minimum, before or after it is stored
+  const int len = max(*static_cast<volatile int*>(lens + b), 0);
+  const int now = keep ? min(len, max(keep[b], 0)) : len;
+  const int last = now / P + (now % P != 0);
+  const int first = window > 0 ? max(0, now - window) / P : 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) lens[b] = now;
+  for (int j = blockIdx.x * kTableThreads + threadIdx.x; j < max_pages; j += gridDim.x * kTableThreads) {
+    if (j >= first && j < last) continue;
+    int* at = table + static_cast<size_t>(b) * max_pages + j;
+    const int p = *at;
+    if (p == -1) continue;
+    *at = -1;
+    if (p >= 0 && p < num_pages) atomicSub(refs + p, 1);
+    else atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+  }
+}
+
+// ==================================================================== copying
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 4;  // 16-byte vectors of a thread in flight
+constexpr size_t kCopyPiece = static_cast<size_t>(kCopyThreads) * kCopyVecs * 16;
+
+// Work items: (move, layer, K or V, piece of a page).
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_kernel(uint4* k, uint4* v, float* ks, float* vs, const int* moves, int room, int layers, int num_pages,
+                int NKV, size_t page_vecs, int pieces) {
+  const int n = min(max(moves[0], 0), room);
+  const long long items = static_cast<long long>(n) * layers * 2 * pieces;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int piece = static_cast<int>(it % pieces);
+    const long long rest = it / pieces;
+    const int w = static_cast<int>(rest & 1);
+    const int layer = static_cast<int>((rest >> 1) % layers);
+    const size_t m = static_cast<size_t>((rest >> 1) / layers);
+    const int src = moves[2 + 2 * m], dst = moves[3 + 2 * m];
+    if (src < 0 || src >= num_pages || dst < 0 || dst >= num_pages) {
+      if (threadIdx.x == 0) atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+      continue;
+    }
+    const size_t base = static_cast<size_t>(layer) * num_pages;
+    uint4* x = w ? v : k;
+    const uint4* from = x + (base + src) * page_vecs;
+    uint4* to = x + (base + dst) * page_vecs;
+    const size_t i0 = piece * (kCopyPiece / 16) + threadIdx.x;
+    uint4 r[kCopyVecs];
+#pragma unroll
+    for (int j = 0; j < kCopyVecs; ++j)
+      if (i0 + j * kCopyThreads < page_vecs) r[j] = from[i0 + j * kCopyThreads];
+#pragma unroll
+    for (int j = 0; j < kCopyVecs; ++j)
+      if (i0 + j * kCopyThreads < page_vecs) to[i0 + j * kCopyThreads] = r[j];
+    if (ks && piece == 0) {
+      float* s = w ? vs : ks;
+      for (int h = threadIdx.x; h < NKV; h += kCopyThreads) s[(base + dst) * NKV + h] = s[(base + src) * NKV + h];
+    }
+  }
+}
+
+int row_blocks(int max_pages) { return std::min((max_pages + kTableThreads - 1) / kTableThreads, 64); }
+
+}  // namespace
+
+cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t stream) {
+  const long long units = a.start ? static_cast<long long>(a.T) / a.P + 2ll * a.B : a.B;
+  append_kernel<<<dim3(static_cast<unsigned>(units), a.NKV, 2), kAppendThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_reserve(int* table, int* lens, int* refs, const int* grow, int* granted, int* moves, int* ws,
+                                 int B, int max_pages, int num_pages, int P, cudaStream_t stream) {
+  reserve_kernel<<<kCluster, kBookThreads, 0, stream>>>(table, lens, refs, grow, granted, moves, ws, B, max_pages,
+                                                        num_pages, P);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const int* table, const int* lens, const int* parent, int* table_out, int* lens_out,
+                              int* refs, int B, int B_out, int max_pages, int num_pages, cudaStream_t stream) {
+  fork_kernel<<<dim3(row_blocks(max_pages), std::max(B, B_out)), kTableThreads, 0, stream>>>(
+      table, lens, parent, table_out, lens_out, refs, B, B_out, max_pages, num_pages);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_free(int* table, int* lens, int* refs, const int* keep, int window, int B, int max_pages,
+                              int num_pages, int P, cudaStream_t stream) {
+  free_kernel<<<dim3(row_blocks(max_pages), B), kTableThreads, 0, stream>>>(table, lens, refs, keep, window, max_pages,
+                                                                            num_pages, P);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(int* table, int* refs, int* moves, int* ws, int B, int max_pages, int num_pages,
+                                 cudaStream_t stream) {
+  compact_kernel<<<kCluster, kBookThreads, 0, stream>>>(refs, moves, ws, num_pages);
+  cudaError_t e = cudaGetLastError();
+  const long long entries = static_cast<long long>(B) * max_pages;
+  if (e != cudaSuccess || entries == 0) return e;
+  const unsigned blocks = static_cast<unsigned>(std::min((entries + kTableThreads - 1) / kTableThreads, 152ll * 8));
+  renumber_kernel<<<blocks, kTableThreads, 0, stream>>>(table, moves, ws, entries, num_pages);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_copy(void* k, void* v, float* ks, float* vs, const int* moves, int room, int layers,
+                              int num_pages, int NKV, size_t page_bytes, cudaStream_t stream) {
+  const int pieces = static_cast<int>((page_bytes + kCopyPiece - 1) / kCopyPiece);
+  const long long items = static_cast<long long>(room) * layers * 2 * pieces;
+  const unsigned blocks = static_cast<unsigned>(std::min(items, 152ll * 8));
+  copy_kernel<<<blocks, kCopyThreads, 0, stream>>>(static_cast<uint4*>(k), static_cast<uint4*>(v), ks, vs, moves, room,
+                                                   layers, num_pages, NKV, page_bytes / 16, pieces);
+  return cudaGetLastError();
+}
+
+cudaError_t read_and_clear_device_error_pages(unsigned int* err) {
+  unsigned int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof v);
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof zero);
+  *err |= v;
+  return e;
+}
+
+}  // namespace fd
