@@ -660,7 +660,7 @@ const char* fd_strerror(int status) {
     case FD_OK: return "ok";
     case FD_ERR_INVALID_ARG: return "invalid argument";
     case FD_ERR_UNSUPPORTED: return "unsupported shape (HS must be 64/128/256/512, NH % NKV == 0, NH/NKV <= 16, "
-                                    "page_size 16/32/64/128, max_pages * page_size < 2^31)";
+                                    "page_size 16/32/64/128, max_pages * page_size < 2^31 - 4096)";
     case FD_ERR_ALIGNMENT: return "pointer not aligned (16 bytes for tensors and workspace, 4 for lens)";
     case FD_ERR_CUDA: return "CUDA runtime call or kernel launch failed";
     case FD_ERR_WORKSPACE: return "workspace too small, or would need allocating while the stream is captured";

@@ -22,6 +22,7 @@ struct PagedArgs {
   const int* lens;         // [B]
   float* ws_o;             // fp32 [2 * blocks][G][HS]
   float* ws_ml;            // fp32 [2 * blocks][G][2]
+  void* cuts;              // [blocks]: the unit that each share's end cuts
   int B, NH, NKV, HS, P, num_pages, max_pages, window;
   int blocks, granule, min_share;
   int kv8;

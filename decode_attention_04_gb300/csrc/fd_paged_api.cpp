@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kMaxGroup = 16;
 constexpr int kMaxHS = 512;
+constexpr int kMaxPositions = INT_MAX - 4096;  // positions are int32, and a tile may reach past the last
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool supported_hs(int HS) { return HS == 64 || HS == 128 || HS == 256 || HS == 512; }
@@ -30,16 +31,18 @@ int check_shape(int B, int NH, int NKV, int HS, int page_size, int max_pages, in
   if (B > 65535 || NKV > 65535) return FD_ERR_INVALID_ARG;
   if (!supported_hs(HS) || !supported_page(page_size)) return FD_ERR_UNSUPPORTED;
   if (NH % NKV != 0 || NH / NKV > kMaxGroup) return FD_ERR_UNSUPPORTED;
-  if (static_cast<long long>(max_pages) * page_size > INT_MAX) return FD_ERR_UNSUPPORTED;  // lens are int32
+  if (static_cast<long long>(max_pages) * page_size > kMaxPositions) return FD_ERR_UNSUPPORTED;  // lens are int32
   return FD_OK;
 }
 
-// Partials: one per share's first and last band, G rows of HS floats, then (m, l).
+// Partials: one per share's first and last band, G rows of HS floats; then
+// their (m, l); then 16 bytes a share on the unit that its end cuts.
 size_t ws_o_bytes(int blocks, int G, int HS) {
   return round_up(static_cast<size_t>(2) * blocks * G * HS * sizeof(float), 256);
 }
+size_t ws_ml_bytes(int blocks, int G) { return round_up(static_cast<size_t>(2) * blocks * G * 2 * sizeof(float), 256); }
 size_t ws_bytes(int blocks, int G, int HS) {
-  return ws_o_bytes(blocks, G, HS) + round_up(static_cast<size_t>(2) * blocks * G * 2 * sizeof(float), 256);
+  return ws_o_bytes(blocks, G, HS) + ws_ml_bytes(blocks, G) + round_up(static_cast<size_t>(blocks) * 16, 256);
 }
 
 int make_plan(int B, int NH, int NKV, int HS, int page_size, int max_pages, int window, int num_sms, int kv_dtype,
@@ -94,6 +97,7 @@ int run(const fd_paged_plan_t& p, void* workspace, size_t workspace_bytes, float
   a.lens = lens;
   a.ws_o = static_cast<float*>(workspace);
   a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws_o_bytes(p.blocks, G, p.HS));
+  a.cuts = reinterpret_cast<char*>(a.ws_ml) + ws_ml_bytes(p.blocks, G);
   a.B = p.B;
   a.NH = p.NH;
   a.NKV = p.NKV;
@@ -300,7 +304,7 @@ int fd_pages_reserve(int* table, int* lens, int* refs, const int* grow, int* gra
                      fd_stream_t stream) {
   const int rc = check_book(B, max_pages, num_pages);
   if (rc != FD_OK) return rc;
-  if (!supported_page(page_size) || static_cast<long long>(max_pages) * page_size > INT_MAX) return FD_ERR_UNSUPPORTED;
+  if (!supported_page(page_size) || static_cast<long long>(max_pages) * page_size > kMaxPositions) return FD_ERR_UNSUPPORTED;
   if (!refs || !moves || (B > 0 && (!table || !lens || !granted))) return FD_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < fd_pages_workspace_bytes(B, num_pages)) return FD_ERR_WORKSPACE;
   if (!aligned(workspace, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(refs, 4) || !aligned(grow, 4) ||
@@ -332,7 +336,7 @@ int fd_pages_free(int* table, int* lens, int* refs, const int* keep, int window,
                   int page_size, fd_stream_t stream) {
   const int rc = check_book(B, max_pages, num_pages);
   if (rc != FD_OK) return rc;
-  if (!supported_page(page_size) || static_cast<long long>(max_pages) * page_size > INT_MAX) return FD_ERR_UNSUPPORTED;
+  if (!supported_page(page_size) || static_cast<long long>(max_pages) * page_size > kMaxPositions) return FD_ERR_UNSUPPORTED;
   if (B == 0) return FD_OK;
   if (!table || !lens || !refs) return FD_ERR_INVALID_ARG;
   if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(refs, 4) || !aligned(keep, 4)) return FD_ERR_ALIGNMENT;

@@ -9,7 +9,7 @@
  *                       E4M3 codes (FD_KV_E4M3)
  *     k_scale, v_scale  fp32 [num_pages][NKV], FD_KV_E4M3 only: a block of
  *                       page_size tokens of one head has one scale for K and
- *                       one for V, value = E4M3(code) * scale
+ *                       one for V, value = E4M3(code) * scale; scales are >= 0
  * Every layer's pool uses the same bookkeeping:
  *     table  int32 [B][max_pages]  page of positions [j * page_size,
  *                                  (j + 1) * page_size) of sequence b; -1: none
@@ -27,7 +27,8 @@
  * whole step can be captured in a CUDA graph.
  *
  * Conventions beside those of fd_decode_attn.h:
- *   - page_size is 16, 32, 64 or 128; HS is 64, 128, 256 or 512.
+ *   - page_size is 16, 32, 64 or 128; HS is 64, 128, 256 or 512;
+ *     max_pages * page_size is below 2^31 - 4096 (else FD_ERR_UNSUPPORTED).
  *   - Tensors are densely packed but for k_new and v_new of fd_paged_append,
  *     whose rows (tokens) may be any multiple of 8 elements apart.
  *   - q, out, the pages, k_new, v_new and workspaces are 16-byte aligned; the
@@ -95,10 +96,10 @@ int fd_paged_plan_sms(int B, int NH, int NKV, int HS, int page_size, int max_pag
  * left out; len_b < 0 counts as 0 (FD_DEVERR_LEN_NEGATIVE); len_b above
  * max_pages * page_size counts as that (FD_DEVERR_LEN_CLAMPED).
  * Arithmetic, E4M3: q is split into two E4M3 terms (exact for elements within
- * 2^14 of the row's largest) and the softmax weights, times their block's V
- * scale, into three (relative error at most 2^-12, or 2^-19 of the largest
- * weight); products accumulate in fp32. bf16: q enters as it is, the weights
- * as two bf16 terms (2^-17).
+ * 2^13 of the row's largest, else off by 2^-21 of that) and the softmax
+ * weights, times their block's V scale, into three (off by 2^-12 of themselves
+ * or 2^-21 of the largest); products accumulate in fp32. bf16: q enters as it
+ * is, the weights as two bf16 terms (2^-16).
  * fd_paged_attn makes its plan for the current device and uses a workspace
  * the library owns, one per (device, stream): the first call for a pair
  * allocates it (not while the stream is captured: FD_ERR_WORKSPACE), large
