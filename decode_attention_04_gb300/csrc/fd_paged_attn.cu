@@ -10,17 +10,20 @@
 // is written to the output directly.
 //
 // A block, per tile of 128 positions (a share's part of one band is a segment):
-//   * Warp 0 brings K and V into a ring of shared-memory slots (one slot: the
+//   * Warps 0 (K) and 11 (V) fill a ring of shared-memory slots (one slot: the
 //     tile's 128 positions x 128 head dims) by TMA, a box of one page's rows
-//     (32 at most) and 128 bytes each; lane i looks up and copies box i. The order
-//     is K(0), then V(i) and K(i + 1) alternately: the scores of the next tile
-//     are computed while the softmax of this one runs.
-//   * Warp 1 issues the MMAs from one thread, out of order between the two
-//     products, accumulators in tensor memory: S^T (positions x query rows) =
-//     K Q^T and O^T (dims x query rows) += V^T P^T. With K as the 128-row
-//     operand the tensor cores read every code once, as it lies in the cache: nothing
-//     is widened.
-//   * Warps 2-5 turn scores into weights, a position a thread.
+//     (32 at most) and 128 bytes each; lane i looks up and copies box i. The ring's order
+//     is K(0), then K(i + 1), V(i): the scores of the next tile are computed while
+//     the softmax of this one runs. A warp spends about 200 cycles on a slot and
+//     70 on each box, so one warp could not fill 16 KB slots at the rate of HBM.
+//   * Warp 1 issues the MMAs in the ring's order, accumulators in tensor
+//     memory: S^T (positions x query rows) = K Q^T and O^T (dims x query rows)
+//     += V^T P^T. With K as the 128-row operand the tensor cores read every code
+//     once, as it lies in the cache: nothing is widened.
+//   * Warps 2-5 and 6-9, two groups, turn scores into weights, a position a
+//     thread: the groups take the tiles in turn, each with an accumulator, a running
+//     maximum and sums of its own, which are joined at the segment's end.
+//   * Warp 10 brings the query rows of the next segments.
 //
 // E4M3 products are exact but for the other operand, which enters as a sum of
 // E4M3 terms, each in MMA columns of its own, term i scaled by 16^i so that it
@@ -182,6 +185,17 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool p) {
   return r != 0;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ------------------------------------------------------------- the division of work
 
 constexpr int kGranule = 32;    // positions
@@ -210,7 +224,7 @@ struct Tile {
   int end;         // positions [max(pos, lo), min(pos + 128, end)) are live in the segment
   int lo;
   int seg;         // number of the segment in this block
-  bool first, last;    // of the segment
+  int j, n;        // tile j of the segment's n
   bool begins, ends;   // the segment holds the band's first / last granule
   bool ok;
 };
@@ -221,7 +235,6 @@ struct Walk {
   int b;
   Band d;
   Tile t;
-  int stop;  // end of the segment, positions
 };
 
 __device__ __forceinline__ Band band_of_seq(const PagedArgs& a, const int* cache, int b) {
@@ -229,10 +242,9 @@ __device__ __forceinline__ Band band_of_seq(const PagedArgs& a, const int* cache
 }
 
 __device__ __forceinline__ void next_tile(const PagedArgs& a, const int* cache, int T, Walk& w) {
-  if (w.t.ok && !w.t.last) {
+  if (w.t.ok && w.t.j + 1 < w.t.n) {
     w.t.pos += T;
-    w.t.first = false;
-    w.t.last = w.t.pos + T >= w.stop;
+    w.t.j += 1;
     return;
   }
   if (w.g >= w.gend) {
@@ -258,19 +270,21 @@ __device__ __forceinline__ void next_tile(const PagedArgs& a, const int* cache, 
   t.ends = g0 + take == w.d.granules;
   // the end of the last granule may lie beyond 2^31 - 1: the band's end does not
   t.end = t.ends ? w.d.len : t.pos + take * kGranule;
-  w.stop = t.end;
-  t.first = true;
-  t.last = t.end - t.pos <= T;
+  t.j = 0;
+  t.n = (t.end - t.pos + T - 1) / T;
   t.ok = true;
 }
 
 // --------------------------------------------------------------------- shapes
 
 constexpr int kTile = 128;     // positions per tile: the M of the score MMA
-constexpr int kSoftWarps = 4;  // one TMEM lane quarter each
-constexpr int W_COPY = 0, W_MMA = 1, W_SOFT0 = 2;
-constexpr int kThreads = (W_SOFT0 + kSoftWarps) * 32;
+constexpr int kSoftWarps = 4;  // of a softmax group: one TMEM lane quarter each
 constexpr int kSoft = kSoftWarps * 32;
+constexpr int W_K = 0, W_MMA = 1, W_SOFT0 = 2, W_Q = W_SOFT0 + 2 * kSoftWarps, W_V = W_Q + 1;
+constexpr int kThreads = (W_V + 1) * 32;
+constexpr int kQRing = 8;      // segments whose query multipliers are kept
+// named barriers
+constexpr int BAR_GROUP = 1, BAR_TMEM = 3, BAR_BOTH = 4;
 
 constexpr int round16(int x) { return (x + 15) / 16 * 16; }
 constexpr int pow2_cols(int x) { return x <= 32 ? 32 : x <= 64 ? 64 : x <= 128 ? 128 : x <= 256 ? 256 : 512; }
@@ -291,32 +305,33 @@ struct Cfg {
   static constexpr int PT = KV8 ? 3 : 2;               // terms of a weight
   static constexpr int NS = round16(QT * NQ);          // columns of S
   static constexpr int NP = round16(PT * NQ);          // columns of O
-  static constexpr int COLS = pow2_cols(2 * NS + NB * NP);
+  static constexpr int COLS = pow2_cols(2 * NS + 2 * NB * NP);
   static constexpr int O_COL = 2 * NS;
   static constexpr int Q_BYTES = NB * CH * NS * SW;
   static constexpr int P_BYTES = NP * kTile * EB;
+  static constexpr int RED_BYTES = 2 * (3 * NQ * kSoftWarps + 2 * NQ) * 4;
   static constexpr int Q_STRIDE = (Q_BYTES + 1023) / 1024 * 1024;
-  static constexpr int RING_ROOM = 227 * 1024 - 2 * Q_STRIDE - 2 * P_BYTES - 3 * NQ * kSoftWarps * 4 - kLenCache * 4 - 2048;
+  static constexpr int RING_ROOM = 227 * 1024 - 2 * Q_STRIDE - 2 * P_BYTES - RED_BYTES - kLenCache * 4 - 2048;
   static constexpr int RING = RING_ROOM / SLOT < 24 ? RING_ROOM / SLOT : 24;  // slots: all the shared memory there is
   static constexpr int OFF_Q = RING * SLOT;
   static constexpr int OFF_P = OFF_Q + 2 * Q_STRIDE;
-  static constexpr int OFF_RED = OFF_P + 2 * P_BYTES;  // f32: [2][NQ][4] tile maxima, [NQ][4] sums
-  static constexpr int OFF_QMUL = OFF_RED + 3 * NQ * kSoftWarps * 4;  // f32 [2][16]
-  static constexpr int OFF_LEN = OFF_QMUL + 2 * 16 * 4;
+  // f32, of each group: [2][NQ][4] tile maxima, [NQ][4] sums; then [2 groups][NQ] (m, l)
+  static constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
+  static constexpr int OFF_QMUL = OFF_RED + RED_BYTES;  // f32 [kQRing][16]
+  static constexpr int OFF_LEN = OFF_QMUL + kQRing * 16 * 4;
   static constexpr int OFF_BAR = OFF_LEN + kLenCache * 4;
-  // full[RING], empty[RING], s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], o_free, mma_done,
-  // v_clean[2][NB]
-  static constexpr int NBAR = 2 * RING + 12 + 2 * NB;
+  // full[RING], empty[RING], s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], q_free[2], o_free[2], mma_done,
+  // v_clean[2][NB], v_here[2][NB]; the pairs by the parity of a tile (its group) or, for q, of a segment
+  static constexpr int NBAR = 2 * RING + 15 + 4 * NB;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tensor memory address; share; edge[2]
   static constexpr int SMEM = OFF_MISC + 64 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(P_BYTES % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms are aligned");
   static_assert(OFF_BAR % 8 == 0, "barriers");
-  static_assert(RING >= 4, "K and V slots pass each other");
-  // Stream position of slot p of tile t's K and V: K(0), then V(i), K(i + 1)
-  // alternately, the last tile's V by itself.
-  static __device__ __forceinline__ int seq_k(int t, int p) { return t == 0 ? p : NB + 2 * NB * (t - 1) + 2 * p + 1; }
-  static __device__ __forceinline__ int seq_v(int t, int p, bool more) { return NB + 2 * NB * t + (more ? 2 * p : p); }
+  static_assert(RING >= 4, "two slots of each of K and V");
+  // Stream position of the first slot of tile t's K and V: K(0), then K(t + 1), V(t).
+  static __device__ __forceinline__ int seq_k(int t) { return t == 0 ? 0 : NB * (2 * t - 1); }
+  static __device__ __forceinline__ int seq_v(int t, bool more) { return NB * (2 * t + (more ? 2 : 1)); }
   // Instruction descriptor: D f32; A and B E4M3 (0) or bf16 (1 in bits 7 and
   // 10); bit 15: A is MN-major; N / 8 at 17, M / 16 at 24.
   static constexpr uint32_t IDESC_QK = (1u << 4) | (KV8 ? 0u : (1u << 7) | (1u << 10)) |
@@ -396,11 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   const int c = blockIdx.x;
   const int G = a.NH / a.NKV;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int page_shift = 31 - __clz(a.P);
 
   const uint32_t bar0 = base + C::OFF_BAR;
   const uint32_t full = bar0, empty = full + 8 * C::RING;
   const uint32_t s_full = empty + 8 * C::RING, s_free = s_full + 16, p_ready = s_free + 16, pv_done = p_ready + 16;
-  const uint32_t q_ready = pv_done + 16, o_free = q_ready + 16, mma_done = o_free + 8, v_clean = mma_done + 8;
+  const uint32_t q_ready = pv_done + 16, q_free = q_ready + 16, o_free = q_free + 16, mma_done = o_free + 16;
+  const uint32_t v_clean = mma_done + 8, v_here = v_clean + 16 * C::NB;
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
   float* qmul = reinterpret_cast<float*>(smem + C::OFF_QMUL);
   int* lens = reinterpret_cast<int*>(smem + C::OFF_LEN);
@@ -420,10 +437,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_init(s_free + 8 * j, kSoft);
       mbar_init(p_ready + 8 * j, kSoft);
       mbar_init(pv_done + 8 * j, 1);
-      mbar_init(q_ready + 8 * j, kSoft);
+      mbar_init(q_ready + 8 * j, 1);
+      mbar_init(q_free + 8 * j, 1);
+      mbar_init(o_free + 8 * j, 2 * kSoft);
     }
-    mbar_init(o_free, kSoft);
-    for (int j = 0; j < 2 * C::NB; ++j) mbar_init(v_clean + 8 * j, kSoft);
+    for (int j = 0; j < 2 * C::NB; ++j) {
+      mbar_init(v_clean + 8 * j, kSoft);
+      mbar_init(v_here + 8 * j, 1);
+    }
     mbar_init(mma_done, 1);
     fence_mbar_init();
     prefetch_tensor_map(&maps.k);
@@ -515,246 +536,248 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   }
 
   bool failed = false;
+  int slots_used = 0;  // of the ring's order, by K and V (the copy warps)
   uint32_t tmem = 0;
-  if (warp >= W_MMA) {
+  if (warp >= W_MMA && warp < W_Q) {
     if (warp == W_MMA) {
       tmem_alloc(base + C::OFF_MISC, C::COLS);
       tmem_relinquish();
     }
     tc_fence_before();
-    named_bar_sync(2, (1 + kSoftWarps) * 32);
+    named_bar_sync(BAR_TMEM, (1 + 2 * kSoftWarps) * 32);
     tc_fence_after();
     tmem = *tmem_at;
   }
 
-  if (warp == W_COPY) {
-    // ------------------------------------------------------------ copy warp
+      // Query rows of a segment -> the B operand of its score MMAs: rows of SW bytes, swizzled,
+      // term j of row r in row j * NQ + r; rows >= G are zero.
+      auto stage_q = [&](const Tile& t, int first, int threads) {
+        const int par = t.seg & 1;
+        unsigned char* qb = smem + C::OFF_Q + par * C::Q_STRIDE;
+        constexpr int EL = 16 / C::EB;           // elements of a 16-byte piece
+        constexpr int PIECES = C::HS / EL;       // of a row: a power of two, at most 64
+        for (int id = first; (id & ~31) < C::NQ * PIECES; id += threads) {  // whole warps
+          const int r = id / PIECES, pc = id % PIECES;
+          const bool live = r < G && r < C::NQ;
+          const int chunk = pc * 16 / C::SW, piece = (pc * 16 % C::SW) / 16;
+          const uint16_t* src = a.q + (static_cast<size_t>(t.b) * a.NH + static_cast<size_t>(t.kvh) * G + r) * C::HS + pc * EL;
+          if constexpr (!C::KV8) {
+            if (r < C::NQ)
+              *reinterpret_cast<uint4*>(qb + chunk * C::NS * C::SW + swizzled<C::SW>(r, piece)) =
+                  live ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+          } else {
+            uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (live) {
+              x[0] = reinterpret_cast<const uint4*>(src)[0];
+              x[1] = reinterpret_cast<const uint4*>(src)[1];
+            }
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(x);
+            float2 f[8];
+            float top = 0.f;
+  #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+              top = fmaxf(top, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
+            }
+            // the row's largest element, over the lanes that hold the row
+  #pragma unroll
+            for (int i = PIECES / 2; i >= 1; i /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+            // times a power of two that brings it to [128, 256); not finite: as it is
+            const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // biased exponent of top >= 0
+            const int sh = (top > 0.f && ex < 255) ? min(7 - (ex - 127), 126) : 0;
+            const float mul = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+            if (pc == 0 && r < C::NQ) qmul[(t.seg & (kQRing - 1)) * 16 + r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+            uint32_t w[2][4];
+  #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float2 y = make_float2(f[i].x * mul, f[i].y * mul);
+              // an infinity would saturate: it has to reach the scores as NaN
+              if (ex == 255) {
+                y.x = isfinite(y.x) ? y.x : __int_as_float(0x7fffffff);
+                y.y = isfinite(y.y) ? y.y : __int_as_float(0x7fffffff);
+              }
+  #pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t term = next_term(y);
+                if (i & 1) w[j][i / 2] |= term << 16;
+                else w[j][i / 2] = term;
+              }
+            }
+            if (r < C::NQ) {
+  #pragma unroll
+              for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<uint4*>(qb + chunk * C::NS * C::SW + swizzled<C::SW>(j * C::NQ + r, piece)) =
+                    make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+      };
+
+  if (warp == W_K || warp == W_V) {
+    // ------------------------------------------------------------ copy warps
+    const CUtensorMap* map = warp == W_K ? &maps.k : &maps.v;
     const int box = min(a.P, 32);           // rows of a copy
     const int nbox = kTile / box;
     const uint32_t box_bytes = box * C::SW * C::CH;
+    const int row = lane * box;             // this lane's box in a tile
     // the table's entry for this lane's box in a tile; -1: nothing to copy
     auto page_of = [&](const Tile& t) {
-      const int r = lane * box;
-      if (!t.ok || lane >= nbox || r >= t.end - t.pos || t.pos + r + box <= t.lo) return -1;
-      return a.table[static_cast<size_t>(t.b) * a.max_pages + (t.pos + r) / a.P];
+      if (!t.ok || lane >= nbox || row >= t.end - t.pos || t.pos + row + box <= t.lo) return -1;
+      return a.table[static_cast<size_t>(t.b) * a.max_pages + ((t.pos + row) >> page_shift)];
     };
     Tile cur = walk.t;
-    int cur_page = page_of(cur);
-    next_tile(a, lens, kTile, walk);
-    Tile nxt = walk.t;
-    int nxt_page = page_of(nxt);
-    int e = 0, slot = 0, use = 0;
-    uint32_t st_issued = 0, st_par = 0;
-    auto copy = [&](const Tile& t, int page, bool is_k, int p) {
-      if (use > 0) mbar_wait(empty + 8 * slot, (use - 1) & 1, failed);
-      const uint32_t fb = full + 8 * slot;
-      const bool there = page >= 0 && page < a.num_pages;
-      const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, there));
-      if (lane == 0) mbar_arrive_expect_tx(fb, boxes * box_bytes);
-      __syncwarp();
-      if (there) {
-        const int r = lane * box;
-        const int y = t.kvh * a.P + (t.pos + r) % a.P;
-#pragma unroll
-        for (int ch = 0; ch < C::CH; ++ch)
-          tma_load_3d(base + slot * C::SLOT + ch * C::CHUNK + r * C::SW, is_k ? &maps.k : &maps.v,
-                      p * C::DB + ch * (C::SW / C::EB), y, page, fb);
-      }
-      st_issued |= 1u << slot;
-      st_par = (st_par & ~(1u << slot)) | (static_cast<uint32_t>(use & 1) << slot);
-      ++e;
-      if (++slot == C::RING) {
-        slot = 0;
-        ++use;
-      }
-    };
-    for (int p = 0; p < C::NB; ++p) copy(cur, cur_page, true, p);
-    while (cur.ok) {
-      // the pages of the tile after the next are looked up while these copies wait for slots
+    int page = page_of(cur);
+    for (int i = 0; cur.ok; ++i) {
       next_tile(a, lens, kTile, walk);
-      const Tile after = walk.t;
-      const int after_page = page_of(after);
+      const Tile nxt = walk.t;
+      const int next_page = page_of(nxt);  // in flight while this tile's copies wait for slots
+      const bool there = page >= 0 && page < a.num_pages;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, there)) * box_bytes;
+      const int y = cur.kvh * a.P + ((cur.pos + row) & (a.P - 1));
+      const int e0 = warp == W_K ? C::seq_k(i) : C::seq_v(i, nxt.ok);
+#pragma unroll
       for (int p = 0; p < C::NB; ++p) {
-        copy(cur, cur_page, false, p);
-        if (nxt.ok) copy(nxt, nxt_page, true, p);
+        const int slot = (e0 + p) % C::RING, use = (e0 + p) / C::RING;
+        if (use > 0) mbar_wait(empty + 8 * slot, (use - 1) & 1, failed);
+        const uint32_t fb = full + 8 * slot;
+        if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
+        __syncwarp();
+        if (there) {
+#pragma unroll
+          for (int ch = 0; ch < C::CH; ++ch)
+            tma_load_3d(base + slot * C::SLOT + ch * C::CHUNK + row * C::SW, map, p * C::DB + ch * (C::SW / C::EB), y,
+                        page, fb);
+        }
       }
       cur = nxt;
-      cur_page = nxt_page;
-      nxt = after;
-      nxt_page = after_page;
+      page = next_page;
+      slots_used += 2 * C::NB;
     }
-    // No copy may be in flight when the block leaves (bounded, own flag).
-    bool dfail = false;
-    for (int k = 0; k < C::RING; ++k)
-      if ((st_issued >> k) & 1u) mbar_wait(full + 8 * k, (st_par >> k) & 1u, dfail);
   } else if (warp == W_MMA) {
-    // ----------------------------------------------------- MMA issue thread
-    if (lane == 0) {
-      Walk vw = walk;
-      int kt = 0, kp = 0, vt = 0, vp = 0;
-      bool s_ok = false, p_ok = false, clear = false;
-      uint32_t cleared = 0;  // bit j: parity of the phase of tiles of parity j
-      uint64_t t_idle = 0;
-      uint32_t spins = 0;  // polls without progress; the clock is read every 4096
-      while (vw.t.ok && !failed) {
-        bool prog = false;
-        if (walk.t.ok) {
-          // the S buffer is free, and the segment's query rows are in place
-          if (!s_ok) s_ok = (kt < 2 || mbar_test(s_free + 8 * (kt & 1), ((kt - 2) >> 1) & 1)) &&
-                            (!walk.t.first || mbar_test(q_ready + 8 * (walk.t.seg & 1), (walk.t.seg >> 1) & 1));
-          const int e = C::seq_k(kt, kp), slot = e % C::RING;
-          if (s_ok && mbar_test(full + 8 * slot, (e / C::RING) & 1)) {
-            tc_fence_after();
-            const uint32_t kb = base + slot * C::SLOT;
-            const uint32_t qb = base + C::OFF_Q + (walk.t.seg & 1) * C::Q_STRIDE + kp * C::CH * C::NS * C::SW;
-#pragma unroll
-            for (int ch = 0; ch < C::CH; ++ch)
-#pragma unroll
-              for (int kk = 0; kk < C::SW / 32; ++kk)
-                umma<C::KV8>(tmem + C::NS * (kt & 1), smem_desc<C::SW>(kb + ch * C::CHUNK + 32 * kk, 16),
-                             smem_desc<C::SW>(qb + ch * C::NS * C::SW + 32 * kk, 16), C::IDESC_QK,
-                             (kp | ch | kk) != 0);
-            umma_commit(empty + 8 * slot);
-            if (++kp == C::NB) {
-              umma_commit(s_full + 8 * (kt & 1));
-              kp = 0;
-              ++kt;
-              s_ok = false;
-              next_tile(a, lens, kTile, walk);
-            }
-            prog = true;
-          }
-        }
-        if (vt < kt) {
-          // the weights are in place, and the segment before has left O
-          if (!p_ok) {
-            p_ok = mbar_test(p_ready + 8 * (vt & 1), (vt >> 1) & 1) &&
-                   (!vw.t.first || vw.t.seg == 0 || mbar_test(o_free, (vw.t.seg - 1) & 1));
-            if (p_ok) clear = edge[vt & 1] != 0;
-          }
-          const int e = C::seq_v(vt, vp, kt > vt + 1 || walk.t.ok), slot = e % C::RING;
-          if (p_ok && mbar_test(full + 8 * slot, (e / C::RING) & 1) && (!clear || mbar_test(v_clean + 8 * ((vt & 1) * C::NB + vp), (cleared >> (vt & 1)) & 1))) {
-            tc_fence_after();
-            const uint32_t vb = base + slot * C::SLOT;
-            const uint32_t pb = base + C::OFF_P + (vt & 1) * C::P_BYTES;
-            const uint32_t d = tmem + C::O_COL + C::NP * vp;
-            const int nk = (min(kTile, vw.t.end - vw.t.pos) + C::KSTEP - 1) / C::KSTEP;
-            for (int kk = 0; kk < nk; ++kk) {
-              const uint32_t pa = pb + kk * 32 / 128 * (C::NP * 128) + kk * 32 % 128;
-              umma<C::KV8>(d, smem_desc<C::SW>(vb + kk * C::KSTEP * C::SW, C::CH > 1 ? C::CHUNK : C::SLOT),
-                           smem_desc<128>(pa, 16), C::IDESC_PV, (!vw.t.first || kk > 0) ? 1u : 0u);
-            }
-            umma_commit(empty + 8 * slot);
-            if (++vp == C::NB) {
-              umma_commit(pv_done + 8 * (vt & 1));
-              if (clear) cleared ^= 1u << (vt & 1);
-              vp = 0;
-              ++vt;
-              p_ok = false;
-              next_tile(a, lens, kTile, vw);
-            }
-            prog = true;
-          }
-        }
-        if (prog) {
-          spins = 0;
-        } else if ((++spins & 4095u) == 0) {
-          const uint64_t now = globaltimer_ns();
-          if (spins == 4096u) {
-            t_idle = now;
-          } else if (now - t_idle > g_wait_limit_ns) {
-            failed = true;
-            atomicOr(&g_device_error, FD_DEVERR_WAIT_TIMEOUT);
-          }
-        }
+    // ------------------------------------------------------------- MMA warp
+    // In the ring's order, the whole warp in step; one lane issues. The
+    // descriptors of a slot differ from those of slot 0 by its address.
+    const bool issuer = elect_one();
+    const uint64_t k_desc = smem_desc<C::SW>(base, 16);
+    const uint64_t v_desc = smem_desc<C::SW>(base, C::CH > 1 ? C::CHUNK : C::SLOT);
+    const uint64_t q_desc = smem_desc<C::SW>(base + C::OFF_Q, 16);
+    const uint64_t p_desc = smem_desc<128>(base + C::OFF_P, 16);
+    int slot = 0;
+    uint32_t turn = 0;  // parity of the ring's turn
+    auto advance = [&] {
+      if (++slot == C::RING) {
+        slot = 0;
+        turn ^= 1;
       }
-      // every MMA issued has completed before the tensor memory is released
-      umma_commit(mma_done);
-      bool dfail = false;
-      mbar_wait(mma_done, 0, dfail);
+    };
+    // bit g, of group g: parity of v_clean's phase, of o_free's, and whether O was used
+    uint32_t cleared = 0, o_phase = 0, o_used = 0;
+    auto scores = [&](int i, const Tile& t) {
+      const int g = i & 1;
+      if (i >= 2) mbar_wait(s_free + 8 * g, ((i - 2) >> 1) & 1, failed);
+      if (t.j == 0) mbar_wait(q_ready + 8 * (t.seg & 1), (t.seg >> 1) & 1, failed);
+      const uint64_t qd = q_desc + (t.seg & 1) * (C::Q_STRIDE >> 4);
+      const uint32_t d = tmem + C::NS * g;
+#pragma unroll
+      for (int p = 0; p < C::NB; ++p) {
+        mbar_wait(full + 8 * slot, turn, failed);
+        tc_fence_after();
+        if (issuer) {
+          const uint64_t kd = k_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
+#pragma unroll
+          for (int ch = 0; ch < C::CH; ++ch)
+#pragma unroll
+            for (int kk = 0; kk < C::SW / 32; ++kk)
+              umma<C::KV8>(d, kd + ((ch * C::CHUNK + 32 * kk) >> 4),
+                           qd + (((p * C::CH + ch) * C::NS * C::SW + 32 * kk) >> 4), C::IDESC_QK, (p | ch | kk) != 0);
+          umma_commit(empty + 8 * slot);
+          if (p == C::NB - 1) {
+            umma_commit(s_full + 8 * g);
+            if (t.j + 1 == t.n) umma_commit(q_free + 8 * (t.seg & 1));
+          }
+        }
+        advance();
+      }
+    };
+    auto values = [&](int i, const Tile& t) {
+      const int g = i & 1;
+      mbar_wait(p_ready + 8 * g, (i >> 1) & 1, failed);
+      if (t.j < 2) {  // the group's first tile of the segment takes O, once the segment before has left it
+        if ((o_used >> g) & 1) {
+          mbar_wait(o_free + 8 * g, (o_phase >> g) & 1, failed);
+          o_phase ^= 1u << g;
+        }
+        o_used |= 1u << g;
+      }
+      const bool clear = edge[g] != 0;
+      const uint64_t pd = p_desc + g * (C::P_BYTES >> 4);
+      const int nk = (min(kTile, t.end - t.pos) + C::KSTEP - 1) / C::KSTEP;
+      const uint32_t keep = t.j > 1 ? 1u : 0u;
+#pragma unroll
+      for (int p = 0; p < C::NB; ++p) {
+        mbar_wait(full + 8 * slot, turn, failed);
+        if (clear) {  // the group clears rows of the slot first
+          if (issuer) mbar_arrive(v_here + 8 * (g * C::NB + p));
+          mbar_wait(v_clean + 8 * (g * C::NB + p), (cleared >> g) & 1, failed);
+        }
+        tc_fence_after();
+        if (issuer) {
+          const uint32_t d = tmem + C::O_COL + C::NP * (g * C::NB + p);
+          const uint64_t vd = v_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kTile / C::KSTEP; ++kk)
+            if (kk < nk)
+              umma<C::KV8>(d, vd + ((kk * C::KSTEP * C::SW) >> 4),
+                           pd + ((kk * 32 / 128 * (C::NP * 128) + kk * 32 % 128) >> 4), C::IDESC_PV, kk > 0 ? 1u : keep);
+          umma_commit(empty + 8 * slot);
+          if (p == C::NB - 1) umma_commit(pv_done + 8 * g);
+        }
+        advance();
+      }
+      if (clear) cleared ^= 1u << g;
+    };
+    Tile cur = walk.t;
+    scores(0, cur);
+    for (int i = 0; cur.ok; ++i) {
+      next_tile(a, lens, kTile, walk);
+      const Tile nxt = walk.t;
+      if (nxt.ok) scores(i + 1, nxt);
+      values(i, cur);
+      cur = nxt;
     }
-    __syncwarp();
+    // every MMA issued has completed before the tensor memory is released
+    if (issuer) umma_commit(mma_done);
+    bool dfail = false;
+    mbar_wait(mma_done, 0, dfail);
+  } else if (warp == W_Q) {
+    // ------------------------------------------------ query rows, from the second segment on
+    for (;;) {
+      if (walk.t.ok) walk.t.j = walk.t.n;  // on to the next segment
+      next_tile(a, lens, kTile, walk);
+      if (!walk.t.ok) break;
+      const int seg = walk.t.seg;
+      if (seg >= 2) mbar_wait(q_free + 8 * (seg & 1), ((seg - 2) >> 1) & 1, failed);
+      stage_q(walk.t, lane, 32);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready + 8 * (seg & 1));
+    }
   } else {
     // ---------------------------------------------- softmax / epilogue warps
     constexpr float kLazy = C::KV8 ? kLazy8 : kLazy16, kBias = C::KV8 ? kBias8 : kBias16;
-    const int sw = warp - W_SOFT0;
+    const int grp = (warp - W_SOFT0) / kSoftWarps;  // takes the tiles i with i % 2 == grp
+    const int sw = (warp - W_SOFT0) % kSoftWarps;
     const int quarter = warp & 3;   // the TMEM lane quarter this warp may access
-    const int tq = tid - W_SOFT0 * 32;
+    const int tq = tid - W_SOFT0 * 32 - grp * kSoft;
     const int pl = quarter * 32 + lane;  // the tile's position whose scores this thread holds
     const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
-
-    // Query rows of a segment -> the B operand of its score MMAs: rows of SW bytes, swizzled,
-    // term j of row r in row j * NQ + r; rows >= G are zero.
-    auto stage_q = [&](const Tile& t) {
-      const int par = t.seg & 1;
-      unsigned char* qb = smem + C::OFF_Q + par * C::Q_STRIDE;
-      constexpr int EL = 16 / C::EB;           // elements of a 16-byte piece
-      constexpr int PIECES = C::HS / EL;       // of a row: a power of two, at most 64
-      for (int id = tq; (id & ~31) < C::NQ * PIECES; id += kSoft) {  // whole warps
-        const int r = id / PIECES, pc = id % PIECES;
-        const bool live = r < G && r < C::NQ;
-        const int chunk = pc * 16 / C::SW, piece = (pc * 16 % C::SW) / 16;
-        const uint16_t* src = a.q + (static_cast<size_t>(t.b) * a.NH + static_cast<size_t>(t.kvh) * G + r) * C::HS + pc * EL;
-        if constexpr (!C::KV8) {
-          if (r < C::NQ)
-            *reinterpret_cast<uint4*>(qb + chunk * C::NS * C::SW + swizzled<C::SW>(r, piece)) =
-                live ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
-        } else {
-          uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-          if (live) {
-            x[0] = reinterpret_cast<const uint4*>(src)[0];
-            x[1] = reinterpret_cast<const uint4*>(src)[1];
-          }
-          const uint32_t* u = reinterpret_cast<const uint32_t*>(x);
-          float2 f[8];
-          float top = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
-            top = fmaxf(top, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
-          }
-          // the row's largest element, over the lanes that hold the row
-#pragma unroll
-          for (int i = PIECES / 2; i >= 1; i /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-          // times a power of two that brings it to [128, 256); not finite: as it is
-          const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // biased exponent of top >= 0
-          const int sh = (top > 0.f && ex < 255) ? min(7 - (ex - 127), 126) : 0;
-          const float mul = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-          if (pc == 0 && r < C::NQ) qmul[par * 16 + r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-          uint32_t w[2][4];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float2 y = make_float2(f[i].x * mul, f[i].y * mul);
-            // an infinity would saturate: it has to reach the scores as NaN
-            if (ex == 255) {
-              y.x = isfinite(y.x) ? y.x : __int_as_float(0x7fffffff);
-              y.y = isfinite(y.y) ? y.y : __int_as_float(0x7fffffff);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t term = next_term(y);
-              if (i & 1) w[j][i / 2] |= term << 16;
-              else w[j][i / 2] = term;
-            }
-          }
-          if (r < C::NQ) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              *reinterpret_cast<uint4*>(qb + chunk * C::NS * C::SW + swizzled<C::SW>(j * C::NQ + r, piece)) =
-                  make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(q_ready + 8 * par);
-    };
 
     // Of this thread's position: the table's entry, two tiles ahead, and the
     // block's scales, one tile ahead: both are in flight while a tile is worked on. -1: the position takes no part.
     auto entry = [&](const Tile& t) {
       const int pos = t.pos + pl;
       if (!t.ok || pl >= t.end - t.pos || pos < t.lo) return -1;
-      return a.table[static_cast<size_t>(t.b) * a.max_pages + pos / a.P];
+      return a.table[static_cast<size_t>(t.b) * a.max_pages + (pos >> page_shift)];
     };
     auto scales = [&](const Tile& t, int page) {
       if (!C::KV8 || page < 0 || page >= a.num_pages) return make_float2(0.f, 0.f);
@@ -762,50 +785,54 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       return make_float2(a.k_scale[at], a.v_scale[at]);
     };
 
+    float* reds = red + grp * 3 * C::NQ * kSoftWarps;
+    float2* stat = reinterpret_cast<float2*>(red + 2 * 3 * C::NQ * kSoftWarps);  // [2][NQ] (m, l)
+    const uint32_t o_cols = tmem + tlane + C::O_COL;
+
+    stage_q(walk.t, tid - W_SOFT0 * 32, 2 * kSoft);
+    named_bar_sync(BAR_BOTH, 2 * kSoft);
+    if (grp == 0 && tq == 0) mbar_arrive(q_ready);
+
+    // This group's tiles: the current one, and whether any tile follows it.
+    if (grp == 1) next_tile(a, lens, kTile, walk);
     Tile cur = walk.t;
     int page = entry(cur);
     next_tile(a, lens, kTile, walk);
+    bool more = walk.t.ok;
+    next_tile(a, lens, kTile, walk);
     Tile nxt = walk.t;
     int next_page = entry(nxt);
-    Walk ahead = walk;  // runs to the first tile of the next segment
-    stage_q(cur);
-    named_bar_sync(1, kSoft);  // qmul
     float2 ksvs = scales(cur, page);
     float m_use[C::NQ], l_part[C::NQ];
-    int i = 0;
+    int i = grp, seg_seen = -1, cleared = 0;
     while (cur.ok) {
+      next_tile(a, lens, kTile, walk);
+      const bool next_more = walk.t.ok;
       next_tile(a, lens, kTile, walk);
       const Tile after = walk.t;
       const int after_page = entry(after);
       const float2 next_ksvs = scales(nxt, next_page);
-      if (cur.first) {
+      const int u = i >> 1;  // number of the tile within the group
+      if (cur.seg != seg_seen) {
+        seg_seen = cur.seg;
 #pragma unroll
         for (int r = 0; r < C::NQ; ++r) {
           m_use[r] = kNegInf;
           l_part[r] = 0.f;
-        }
-        // The next segment's query rows; their buffer was last read by the scores of
-        // the segment before this one, which have been waited for.
-        if (ahead.t.ok && !ahead.t.first) {
-          ahead.t.last = true;
-          next_tile(a, lens, kTile, ahead);
-        }
-        if (ahead.t.ok) {
-          stage_q(ahead.t);
-          next_tile(a, lens, kTile, ahead);
         }
       }
       const bool live = page >= 0 && page < a.num_pages;
       const int rows = (min(kTile, cur.end - cur.pos) + C::KSTEP - 1) / C::KSTEP * C::KSTEP;  // that P.V reads
       const bool dead_row = !live && pl < rows;
       if (dead_row && cur.pos + pl >= cur.lo && cur.pos + pl < cur.end) atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
-      mbar_wait(s_full + 8 * (i & 1), (i >> 1) & 1, failed);
+      mbar_wait(s_full + 8 * grp, u & 1, failed);
       tc_fence_after();
       float s[C::NS];
-      tmem_load<C::NS>(tmem + tlane + C::NS * (i & 1), s);
+      tmem_load<C::NS>(tmem + tlane + C::NS * grp, s);
       tc_fence_before();
-      mbar_arrive(s_free + 8 * (i & 1));
+      mbar_arrive(s_free + 8 * grp);
 
+      // the segment's multipliers were in place before its score MMAs were issued
       // sc: log2 of the weight for the row's sum; sc + lvs: for the product with V's codes
       float sc[C::NQ], t[C::NQ];
       float lvs = 0.f;
@@ -814,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         lvs = ksvs.y == 0.f ? -150.f : log2f(ksvs.y);
 #pragma unroll
         for (int r = 0; r < C::NQ; ++r)
-          sc[r] = (s[r] + s[C::NQ + r] * 0.0625f) * (ksvs.x * qmul[(cur.seg & 1) * 16 + r]);
+          sc[r] = (s[r] + s[C::NQ + r] * 0.0625f) * (ksvs.x * qmul[(cur.seg & (kQRing - 1)) * 16 + r]);
       } else {
 #pragma unroll
         for (int r = 0; r < C::NQ; ++r) sc[r] = s[r] * a.scale_log2;
@@ -825,11 +852,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         t[r] = sc[r] + lvs;
       }
       // the tile's row maxima: warp butterfly, then the four warps' values
-      float* rm = red + (i & 1) * C::NQ * kSoftWarps;
+      float* rm = reds + (u & 1) * C::NQ * kSoftWarps;
       const float wmax = rowreduce<C::NQ>(t, lane, MaxOp());
       constexpr int kPer = 32 / C::NQ;  // lanes that end with the same row
       if (lane % kPer == 0) rm[(lane / kPer) * kSoftWarps + sw] = wmax;
-      const bool clear = named_bar_or(1, kSoft, dead_row);  // the same for every thread
+      const bool clear = named_bar_or(BAR_GROUP + grp, kSoft, dead_row);  // the same for every thread
       bool resc = false;
       float alpha[C::NQ];
 #pragma unroll
@@ -845,17 +872,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       if (resc) {
 #pragma unroll
         for (int r = 0; r < C::NQ; ++r) l_part[r] *= alpha[r];
-        if (!cur.first) {  // O holds the segment's earlier tiles: rescale it once P.V(i - 1) is done
-          mbar_wait(pv_done + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, failed);
+        if (cur.j > 1) {  // O holds the group's earlier tiles of the segment: rescale it once they are done
+          mbar_wait(pv_done + 8 * grp, (u - 1) & 1, failed);
           tc_fence_after();
 #pragma unroll
-          for (int mb = 0; mb < C::NB; ++mb) {
-            float o[C::NP];
-            tmem_load<C::NP>(tmem + tlane + C::O_COL + C::NP * mb, o);
+          for (int x = 0; x < C::NB * C::NP; x += 16) {
+            // 16 columns: of NQ = 16 rows one term, of fewer rows several
+            float o[16];
+            tmem_load<16>(o_cols + C::NP * C::NB * grp + x, o);
 #pragma unroll
-            for (int r = 0; r < C::PT * C::NQ; ++r) o[r] *= alpha[r % C::NQ];
-#pragma unroll
-            for (int j = 0; j < C::NP; j += 16) tmem_st16(tmem + tlane + C::O_COL + C::NP * mb + j, o + j);
+            for (int r = 0; r < 16; ++r) o[r] *= alpha[r % C::NQ];
+            tmem_st16(o_cols + C::NP * C::NB * grp + x, o);
           }
           tmem_st_wait();
         }
@@ -868,10 +895,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         l_part[r] += C::KV8 ? exp2f(sc[r] - ref) : w[r];
       }
 
-      // P(i) -> buffer i % 2; its last reader, P.V(i - 2), must be done
-      if (i >= 2) mbar_wait(pv_done + 8 * (i & 1), ((i - 2) >> 1) & 1, failed);
-      if (tq == 0) edge[i & 1] = clear;
-      unsigned char* pbuf = smem + C::OFF_P + (i & 1) * C::P_BYTES;
+      // P(i) -> the group's buffer; its last reader, P.V(i - 2), must be done
+      if (u >= 1) mbar_wait(pv_done + 8 * grp, (u - 1) & 1, failed);
+      if (tq == 0) edge[grp] = clear;
+      unsigned char* pbuf = smem + C::OFF_P + grp * C::P_BYTES;
       if constexpr (C::KV8) {
 #pragma unroll
         for (int r = 0; r < C::NQ; r += 2) {
@@ -897,76 +924,119 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       }
       fence_proxy_async_smem();  // P -> the tensor cores' view of shared memory
       tc_fence_before();
-      mbar_arrive(p_ready + 8 * (i & 1));
+      mbar_arrive(p_ready + 8 * grp);
 
       // A position that takes no part has weight 0, but its V row may hold
       // anything, NaN too: it is cleared before the MMAs read the slot.
       if (clear) {
         for (int p = 0; p < C::NB; ++p) {
-          const int e = C::seq_v(i, p, nxt.ok), slot = e % C::RING;
-          mbar_wait(full + 8 * slot, (e / C::RING) & 1, failed);
+          const int slot = (C::seq_v(i, more) + p) % C::RING;
+          mbar_wait(v_here + 8 * (grp * C::NB + p), cleared & 1, failed);
           if (dead_row) {
             for (int ch = 0; ch < C::CH; ++ch)
               for (int x = 0; x < C::SW; x += 16)
                 *reinterpret_cast<uint4*>(smem + slot * C::SLOT + ch * C::CHUNK + pl * C::SW + x) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
-          mbar_arrive(v_clean + 8 * ((i & 1) * C::NB + p));
+          mbar_arrive(v_clean + 8 * (grp * C::NB + p));
         }
+        ++cleared;
       }
 
-      if (cur.last) {
-        // ---- epilogue: the row sums, then this thread's dim of each block of dims
-        float* rs = red + 2 * C::NQ * kSoftWarps;
+      if (cur.j + 2 >= cur.n) {
+        // ---- epilogue, after the group's last tile of the segment: its row sums, then this thread's
+        // dim of blocks of dims. Where both groups had tiles they exchange (m, l), and each takes half
+        // of the output from both accumulators.
+        const bool both = cur.n > 1;
+        float* rs = reds + 2 * C::NQ * kSoftWarps;
         const float lsum = rowreduce<C::NQ>(l_part, lane, AddOp());
-        named_bar_sync(1, kSoft);  // the last segment's sums have been read
         if (lane % kPer == 0) rs[(lane / kPer) * kSoftWarps + sw] = lsum;
-        named_bar_sync(1, kSoft);
-        float L[C::NQ];
+        named_bar_sync(BAR_GROUP + grp, kSoft);
+        mbar_wait(pv_done + 8 * grp, u & 1, failed);
+        if (tq < C::NQ) {
+          const float4 t4 = *reinterpret_cast<const float4*>(rs + tq * kSoftWarps);
+          float mr = m_use[0];
 #pragma unroll
-        for (int r = 0; r < C::NQ; ++r) {
-          const float4 t4 = *reinterpret_cast<const float4*>(rs + r * kSoftWarps);
-          L[r] = (t4.x + t4.y) + (t4.z + t4.w);  // fixed order
+          for (int r = 1; r < C::NQ; ++r)
+            if (r == tq) mr = m_use[r];
+          stat[grp * C::NQ + tq] = make_float2(mr, (t4.x + t4.y) + (t4.z + t4.w));  // fixed order
         }
+        if (both) named_bar_sync(BAR_BOTH, 2 * kSoft);
+        else named_bar_sync(BAR_GROUP + grp, kSoft);
+        tc_fence_after();
         const bool direct = cur.begins && cur.ends;
         const int slot = 2 * c + (cur.begins ? 1 : 0);
-        mbar_wait(pv_done + 8 * (i & 1), (i >> 1) & 1, failed);
-        tc_fence_after();
 #pragma unroll
         for (int mb = 0; mb < C::NB; ++mb) {
-          float o[C::NP];
-          tmem_load<C::NP>(tmem + tlane + C::O_COL + C::NP * mb, o);
+          if (both && C::NB > 1 && (mb & 1) != grp) continue;
+          // with one block of dims the groups share its rows
+          const int row0 = both && C::NB == 1 ? grp * (C::NQ / 2) : 0;
+          const int row1 = both && C::NB == 1 ? row0 + C::NQ / 2 : C::NQ;
+          float x[C::NQ];
+#pragma unroll
+          for (int r = 0; r < C::NQ; ++r) x[r] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {  // the groups' accumulators, in fixed order
+            if (!both && k != grp) continue;
+            float f[C::NQ];
+#pragma unroll
+            for (int r = 0; r < C::NQ; ++r) {
+              const float m0 = stat[r].x, m1 = stat[C::NQ + r].x, m = fmaxf(m0, m1);
+              f[r] = !both ? 1.f : m == kNegInf ? 1.f : exp2f((k ? m1 : m0) - m);
+            }
+            const uint32_t at = o_cols + C::NP * (C::NB * k + mb);
+            if constexpr (C::NQ == 16) {
+#pragma unroll
+              for (int term = 0; term < C::PT; ++term) {
+                float o[16];
+                tmem_load<16>(at + 16 * term, o);
+                const float by = !C::KV8 || term == 0 ? 1.f : term == 1 ? 0.0625f : 0.00390625f;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[r] += f[r] * by * o[r];
+              }
+            } else {
+              float o[C::NP];
+              tmem_load<C::NP>(at, o);
+#pragma unroll
+              for (int r = 0; r < C::NQ; ++r)
+                x[r] += f[r] * (C::KV8 ? o[r] + (o[C::NQ + r] + o[(C::PT - 1) * C::NQ + r] * 0.0625f) * 0.0625f
+                                       : o[r] + o[C::NQ + r]);
+            }
+          }
           const int d = mb * 128 + pl;  // O^T lanes are head dims
           if (pl < C::DB) {
 #pragma unroll
             for (int r = 0; r < C::NQ; ++r) {
               if (r >= G) break;
-              const float x = C::KV8 ? o[r] + (o[C::NQ + r] + o[(C::PT - 1) * C::NQ + r] * 0.0625f) * 0.0625f
-                                     : o[r] + o[C::NQ + r];
+              if (r < row0 || r >= row1) continue;
               if (direct) {
+                const float2 s0 = stat[(both ? 0 : grp) * C::NQ + r], s1 = stat[C::NQ + r];
+                const float m = fmaxf(s0.x, s1.x);
+                const float L = !both ? s0.y : m == kNegInf ? s0.y + s1.y : exp2f(s0.x - m) * s0.y + exp2f(s1.x - m) * s1.y;
                 const size_t at = (static_cast<size_t>(cur.b) * a.NH + static_cast<size_t>(cur.kvh) * G + r) * C::HS + d;
-                const float y = L[r] == 0.f ? 0.f : x / L[r];
+                const float y = L == 0.f ? 0.f : x[r] / L;
                 a.out[at] = f32_to_bf16_bits(y);
                 if (a.out_f32) a.out_f32[at] = y;
               } else {
-                a.ws_o[(static_cast<size_t>(slot) * G + r) * C::HS + d] = x;
+                a.ws_o[(static_cast<size_t>(slot) * G + r) * C::HS + d] = x[r];
               }
             }
           }
         }
-        tc_fence_before();
-        mbar_arrive(o_free);  // the next segment may use O
-        if (!direct && tq < G) {
-          float mr = m_use[0], lr = L[0];
-#pragma unroll
-          for (int r = 1; r < C::NQ; ++r)
-            if (r == tq) {
-              mr = m_use[r];
-              lr = L[r];
-            }
-          reinterpret_cast<float2*>(a.ws_ml)[static_cast<size_t>(slot) * G + tq] = make_float2(mr, lr);
+        if (!direct && tq < G && (!both || grp == 0)) {
+          const float2 s0 = stat[(both ? 0 : grp) * C::NQ + tq], s1 = stat[C::NQ + tq];
+          const float m = fmaxf(s0.x, s1.x);
+          reinterpret_cast<float2*>(a.ws_ml)[static_cast<size_t>(slot) * G + tq] =
+              !both ? s0
+              : m == kNegInf
+                  ? make_float2(m, s0.y + s1.y)
+                  : make_float2(m, exp2f(s0.x - m) * s0.y + exp2f(s1.x - m) * s1.y);
         }
-        if (!nxt.ok && tq == 0) {
+        // the accumulators are free for the next segment (256 arrivals each)
+        tc_fence_before();
+        mbar_arrive(o_free + 8 * grp);
+        mbar_arrive(o_free + 8 * (both ? 1 - grp : grp));
+        if (cur.j + 1 == cur.n && !more && tq == 0) {  // the block's last tile
           Cut cut{cur.b, cur.kvh, -1, -1};
           if (!cur.ends) {
             const Band d = band_of_seq(a, lens, cur.b);
@@ -977,12 +1047,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           cuts[c] = cut;
         }
       }
+      more = next_more;
       cur = nxt;
       page = next_page;
       ksvs = next_ksvs;
       nxt = after;
       next_page = after_page;
-      ++i;
+      i += 2;
     }
   }
 
@@ -992,6 +1063,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   if (warp == W_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, C::COLS);
+  }
+  // No copy may be in flight when the block leaves, also where a wait gave up:
+  // the last phase of each slot (bounded, own flag).
+  if (warp == W_V) {
+    bool dfail = false;
+    for (int k = 0; k < C::RING && k < slots_used; ++k)
+      mbar_wait(full + 8 * k, ((slots_used - 1 - k) / C::RING) & 1, dfail);
   }
 }
 
