@@ -198,11 +198,13 @@ __device__ __forceinline__ bool elect_one() {
 
 // ------------------------------------------------------------- the division of work
 
+constexpr int kTile = 128;      // positions per tile: the M of the score MMA
 constexpr int kGranule = 32;    // positions
 constexpr int kLenCache = 1024; // lengths kept in shared memory when there are no more sequences
 
 struct Band {
-  int len, lo, granules;  // live positions [lo, len), counted in granules from floor(lo / 32)
+  unsigned lo;
+  int len, granules;  // live positions [lo, len), counted in granules from floor(lo / 32)
 };
 
 __device__ __forceinline__ int clamp_len(const PagedArgs& a, int len) {
@@ -212,8 +214,8 @@ __device__ __forceinline__ int clamp_len(const PagedArgs& a, int len) {
 __device__ __forceinline__ Band band_from(const PagedArgs& a, int len) {
   Band d;
   d.len = len;
-  d.lo = a.window > 0 ? max(0, len - a.window) : 0;
-  d.granules = len > 0 ? (len - 1) / kGranule - d.lo / kGranule + 1 : 0;
+  d.lo = a.window > 0 ? max(0, len - a.window) : 0u;
+  d.granules = len > 0 ? static_cast<int>((len - 1u) / kGranule - d.lo / kGranule + 1) : 0;
   return d;
 }
 
@@ -231,9 +233,9 @@ struct Tile {
 
 // Walks a block's tiles in order.
 struct Walk {
-  long long g, gend, off;  // granules: next one, the share's end, where sequence b's units begin
-  int b;
-  Band d;
+  long long left;  // granules of the share that are still to come
+  int kvh, g0;     // where the next segment begins: head, granule of the band
+  Band d;          // of sequence t.b
   Tile t;
 };
 
@@ -241,43 +243,42 @@ __device__ __forceinline__ Band band_of_seq(const PagedArgs& a, const int* cache
   return band_from(a, a.B <= kLenCache ? cache[b] : clamp_len(a, a.lens[b]));
 }
 
-__device__ __forceinline__ void next_tile(const PagedArgs& a, const int* cache, int T, Walk& w) {
-  if (w.t.ok && w.t.j + 1 < w.t.n) {
-    w.t.pos += T;
-    w.t.j += 1;
-    return;
-  }
-  if (w.g >= w.gend) {
-    w.t.ok = false;
-    return;
-  }
-  while (w.g >= w.off + static_cast<long long>(a.NKV) * w.d.granules) {
-    w.off += static_cast<long long>(a.NKV) * w.d.granules;
-    w.d = band_of_seq(a, cache, ++w.b);
-  }
-  const long long in = w.g - w.off;
-  const int kvh = static_cast<int>(in / w.d.granules);
-  const int g0 = static_cast<int>(in - static_cast<long long>(kvh) * w.d.granules);
-  const int take = static_cast<int>(min(static_cast<long long>(w.d.granules - g0), w.gend - w.g));
-  w.g += take;
+__device__ __forceinline__ void next_tile(const PagedArgs& a, const int* cache, Walk& w) {
   Tile& t = w.t;
+  if (t.j + 1 < t.n) {
+    t.pos += kTile;
+    t.j += 1;
+    return;
+  }
+  if (w.left <= 0) {
+    t.ok = false;
+    t.n = 0;
+    return;
+  }
+  while (w.g0 >= w.d.granules) {  // the band is done: the next head, or the next sequence that has one
+    w.g0 = 0;
+    if (++w.kvh >= a.NKV || w.d.granules == 0) {
+      w.kvh = 0;
+      w.d = band_of_seq(a, cache, ++t.b);
+    }
+  }
+  const int take = static_cast<int>(min(static_cast<long long>(w.d.granules - w.g0), w.left));
+  w.left -= take;
   t.seg += 1;
-  t.b = w.b;
-  t.kvh = kvh;
+  t.kvh = w.kvh;
   t.lo = w.d.lo;
-  t.pos = (w.d.lo / kGranule + g0) * kGranule;
-  t.begins = g0 == 0;
-  t.ends = g0 + take == w.d.granules;
-  // the end of the last granule may lie beyond 2^31 - 1: the band's end does not
+  t.pos = (w.d.lo / kGranule + w.g0) * kGranule;
+  t.begins = w.g0 == 0;
+  w.g0 += take;
+  t.ends = w.g0 == w.d.granules;
   t.end = t.ends ? w.d.len : t.pos + take * kGranule;
   t.j = 0;
-  t.n = (t.end - t.pos + T - 1) / T;
+  t.n = (t.end - t.pos + kTile - 1) / kTile;
   t.ok = true;
 }
 
 // --------------------------------------------------------------------- shapes
 
-constexpr int kTile = 128;     // positions per tile: the M of the score MMA
 constexpr int kSoftWarps = 4;  // of a softmax group: one TMEM lane quarter each
 constexpr int kSoft = kSoftWarps * 32;
 constexpr int W_K = 0, W_MMA = 1, W_SOFT0 = 2, W_Q = W_SOFT0 + 2 * kSoftWarps, W_V = W_Q + 1;
@@ -309,13 +310,13 @@ struct Cfg {
   static constexpr int O_COL = 2 * NS;
   static constexpr int Q_BYTES = NB * CH * NS * SW;
   static constexpr int P_BYTES = NP * kTile * EB;
-  static constexpr int RED_BYTES = 2 * (3 * NQ * kSoftWarps + 2 * NQ) * 4;
+  static constexpr int RED_BYTES = (2 * 11 + 4) * NQ * 4;
   static constexpr int Q_STRIDE = (Q_BYTES + 1023) / 1024 * 1024;
   static constexpr int RING_ROOM = 227 * 1024 - 2 * Q_STRIDE - 2 * P_BYTES - RED_BYTES - kLenCache * 4 - 2048;
   static constexpr int RING = RING_ROOM / SLOT < 24 ? RING_ROOM / SLOT : 24;  // slots: all the shared memory there is
   static constexpr int OFF_Q = RING * SLOT;
   static constexpr int OFF_P = OFF_Q + 2 * Q_STRIDE;
-  // f32, of each group: [2][NQ][4] tile maxima, [NQ][4] sums; then [2 groups][NQ] (m, l)
+  // f32, of each group 11 NQ, of both 4 NQ: the groups' statistics
   static constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
   static constexpr int OFF_QMUL = OFF_RED + RED_BYTES;  // f32 [kQRing][16]
   static constexpr int OFF_LEN = OFF_QMUL + kQRing * 16 * 4;
@@ -422,9 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   float* qmul = reinterpret_cast<float*>(smem + C::OFF_QMUL);
   int* lens = reinterpret_cast<int*>(smem + C::OFF_LEN);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
-  long long* share = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);  // per, off of b0, total
-  int* share_b = reinterpret_cast<int*>(smem + C::OFF_MISC + 40);
-  volatile int* edge = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 48);  // of tile i: V has rows to clear
+  long long* share = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);  // granules: per share, all; before the first band
+  int* share_at = reinterpret_cast<int*>(smem + C::OFF_MISC + 40);  // where the share begins: sequence, head, granule
+  volatile int* edge = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 52);  // of tile i: V has rows to clear
 
   // Set-up that reads no input, overlapping the previous kernel's tail.
   if (tid == 0) {
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     const long long start = per * c;
     if (tid == 0) {
       share[0] = per;
-      share[2] = total;
+      share[1] = total;
     }
     long long before = 0;  // granules (of one head) of the sequences before this chunk
     for (int b0 = 0; b0 < a.B && start < total; b0 += kThreads) {
@@ -498,26 +499,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       }
       const long long off = (before + inc - x) * a.NKV;
       if (x > 0 && off <= start && start < off + x * a.NKV) {
-        share[1] = off;
-        *share_b = b;
+        share[2] = off;
+        share_at[0] = b;
+        share_at[1] = static_cast<int>((start - off) / x);
+        share_at[2] = static_cast<int>((start - off) % x);
       }
       before += all;
       if (start < before * a.NKV) break;
     }
     __syncthreads();
   }
-  const long long per = share[0], total = share[2];
+  const long long per = share[0], total = share[1];
   Walk walk;
-  walk.g = min(per * c, total);
-  walk.gend = min(per * (c + 1), total);
+  walk.left = min(per, total - per * c);
   walk.t.ok = false;
   walk.t.seg = -1;
-  const bool work = walk.g < walk.gend;
+  walk.t.j = walk.t.n = 0;
+  const bool work = walk.left > 0;
   if (work) {
-    walk.off = share[1];
-    walk.b = *share_b;
-    walk.d = band_of_seq(a, lens, walk.b);
-    next_tile(a, lens, kTile, walk);
+    walk.t.b = share_at[0];
+    walk.kvh = share_at[1];
+    walk.g0 = share_at[2];
+    walk.d = band_of_seq(a, lens, walk.t.b);
+    next_tile(a, lens, walk);
   }
 
   // Rows of empty sequences are zero.
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     Tile cur = walk.t;
     int page = page_of(cur);
     for (int i = 0; cur.ok; ++i) {
-      next_tile(a, lens, kTile, walk);
+      next_tile(a, lens, walk);
       const Tile nxt = walk.t;
       const int next_page = page_of(nxt);  // in flight while this tile's copies wait for slots
       const bool there = page >= 0 && page < a.num_pages;
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     Tile cur = walk.t;
     scores(0, cur);
     for (int i = 0; cur.ok; ++i) {
-      next_tile(a, lens, kTile, walk);
+      next_tile(a, lens, walk);
       const Tile nxt = walk.t;
       if (nxt.ok) scores(i + 1, nxt);
       values(i, cur);
@@ -753,14 +757,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   } else if (warp == W_Q) {
     // ------------------------------------------------ query rows, from the second segment on
     for (;;) {
-      if (walk.t.ok) walk.t.j = walk.t.n;  // on to the next segment
-      next_tile(a, lens, kTile, walk);
+      walk.t.j = walk.t.n;  // on to the next segment
+      next_tile(a, lens, walk);
       if (!walk.t.ok) break;
       const int seg = walk.t.seg;
       if (seg >= 2) mbar_wait(q_free + 8 * (seg & 1), ((seg - 2) >> 1) & 1, failed);
       stage_q(walk.t, lane, 32);
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready + 8 * (seg & 1));
+    }
+    // the unit that the share's end cuts, if it does: for the merge
+    if (lane == 0) {
+      Cut cut{walk.t.b, walk.t.kvh, -1, -1};
+      if (!walk.t.ends) {
+        const long long u0 = per * (c + 1) - walk.g0;  // a share that ends inside a band is a full one
+        cut.c0 = static_cast<int>(u0 / per);
+        cut.c1 = static_cast<int>((u0 + walk.d.granules - 1) / per);
+      }
+      cuts[c] = cut;
     }
   } else {
     // ---------------------------------------------- softmax / epilogue warps
@@ -785,46 +799,57 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       return make_float2(a.k_scale[at], a.v_scale[at]);
     };
 
-    float* reds = red + grp * 3 * C::NQ * kSoftWarps;
-    float2* stat = reinterpret_cast<float2*>(red + 2 * 3 * C::NQ * kSoftWarps);  // [2][NQ] (m, l)
+    // Shared memory of the group: [NQ][4] maxima, [NQ][4] sums, [NQ] references, [2][NQ] factors of
+    // the accumulators; of both groups: [2][NQ] (reference, sum).
+    float* part = red + grp * 11 * C::NQ;
+    float* sums = part + 4 * C::NQ;
+    float* refs = sums + 4 * C::NQ;
+    float* fac = refs + C::NQ;
+    float2* stat = reinterpret_cast<float2*>(red + 2 * 11 * C::NQ);
     const uint32_t o_cols = tmem + tlane + C::O_COL;
 
     stage_q(walk.t, tid - W_SOFT0 * 32, 2 * kSoft);
     named_bar_sync(BAR_BOTH, 2 * kSoft);
     if (grp == 0 && tq == 0) mbar_arrive(q_ready);
 
-    // This group's tiles: the current one, and whether any tile follows it.
-    if (grp == 1) next_tile(a, lens, kTile, walk);
+    // This group's tiles: the current one and the next. `more`: some tile follows the current one.
+    if (grp == 1) next_tile(a, lens, walk);
     Tile cur = walk.t;
     int page = entry(cur);
-    next_tile(a, lens, kTile, walk);
+    next_tile(a, lens, walk);
     bool more = walk.t.ok;
-    next_tile(a, lens, kTile, walk);
+    next_tile(a, lens, walk);
     Tile nxt = walk.t;
     int next_page = entry(nxt);
     float2 ksvs = scales(cur, page);
-    float m_use[C::NQ], l_part[C::NQ];
+    // Per row: the reference (the running maximum less the bias), this thread's share of the sum. A lane
+    // also keeps the reference of the row that it ends with in a row reduction.
+    constexpr float kNone = -3e38f;  // below every score
+    constexpr int kPer = 32 / C::NQ; // lanes that end with the same row
+    float ref[C::NQ], l_part[C::NQ];
+    float ref_lane = kNone;
     int i = grp, seg_seen = -1, cleared = 0;
     while (cur.ok) {
-      next_tile(a, lens, kTile, walk);
+      next_tile(a, lens, walk);
       const bool next_more = walk.t.ok;
-      next_tile(a, lens, kTile, walk);
+      next_tile(a, lens, walk);
       const Tile after = walk.t;
       const int after_page = entry(after);
       const float2 next_ksvs = scales(nxt, next_page);
       const int u = i >> 1;  // number of the tile within the group
       if (cur.seg != seg_seen) {
         seg_seen = cur.seg;
+        ref_lane = kNone;
 #pragma unroll
         for (int r = 0; r < C::NQ; ++r) {
-          m_use[r] = kNegInf;
+          ref[r] = kNone;
           l_part[r] = 0.f;
         }
       }
       const bool live = page >= 0 && page < a.num_pages;
       const int rows = (min(kTile, cur.end - cur.pos) + C::KSTEP - 1) / C::KSTEP * C::KSTEP;  // that P.V reads
       const bool dead_row = !live && pl < rows;
-      if (dead_row && cur.pos + pl >= cur.lo && cur.pos + pl < cur.end) atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+
       mbar_wait(s_full + 8 * grp, u & 1, failed);
       tc_fence_after();
       float s[C::NS];
@@ -833,49 +858,57 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_arrive(s_free + 8 * grp);
 
       // the segment's multipliers were in place before its score MMAs were issued
-      // sc: log2 of the weight for the row's sum; sc + lvs: for the product with V's codes
+      // sc: log2 of the weight for the row's sum; t: for the product with V's codes
       float sc[C::NQ], t[C::NQ];
-      float lvs = 0.f;
       if constexpr (C::KV8) {
         // a scale of 0 counts as 2^-150: its weights vanish beside any other's
-        lvs = ksvs.y == 0.f ? -150.f : log2f(ksvs.y);
+        const float lvs = ksvs.y == 0.f ? -150.f : log2f(ksvs.y);
+        const float4* qm = reinterpret_cast<const float4*>(qmul + (cur.seg & (kQRing - 1)) * 16);
 #pragma unroll
-        for (int r = 0; r < C::NQ; ++r)
-          sc[r] = (s[r] + s[C::NQ + r] * 0.0625f) * (ksvs.x * qmul[(cur.seg & (kQRing - 1)) * 16 + r]);
+        for (int r = 0; r < C::NQ; r += 4) {
+          const float4 m = qm[r / 4];
+          const float mul[4] = {ksvs.x * m.x, ksvs.x * m.y, ksvs.x * m.z, ksvs.x * m.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sc[r + j] = live ? (s[r + j] + s[C::NQ + r + j] * 0.0625f) * mul[j] : kNegInf;
+            t[r + j] = sc[r + j] + lvs;
+          }
+        }
       } else {
 #pragma unroll
-        for (int r = 0; r < C::NQ; ++r) sc[r] = s[r] * a.scale_log2;
+        for (int r = 0; r < C::NQ; ++r) t[r] = sc[r] = live ? s[r] * a.scale_log2 : kNegInf;
       }
-#pragma unroll
-      for (int r = 0; r < C::NQ; ++r) {
-        sc[r] = live ? sc[r] : kNegInf;
-        t[r] = sc[r] + lvs;
-      }
-      // the tile's row maxima: warp butterfly, then the four warps' values
-      float* rm = reds + (u & 1) * C::NQ * kSoftWarps;
+      // The tile's row maxima. Most tiles move no reference and have every row live: one
+      // barrier tells the group so.
       const float wmax = rowreduce<C::NQ>(t, lane, MaxOp());
-      constexpr int kPer = 32 / C::NQ;  // lanes that end with the same row
-      if (lane % kPer == 0) rm[(lane / kPer) * kSoftWarps + sw] = wmax;
-      const bool clear = named_bar_or(BAR_GROUP + grp, kSoft, dead_row);  // the same for every thread
-      bool resc = false;
-      float alpha[C::NQ];
+      bool clear = false;
+      if (named_bar_or(BAR_GROUP + grp, kSoft, dead_row || wmax > ref_lane + (kLazy + kBias))) {
+        if (dead_row && cur.pos + pl >= cur.lo && cur.pos + pl < cur.end) atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
+        if (lane % kPer == 0) part[(lane / kPer) * kSoftWarps + sw] = wmax;
+        clear = named_bar_or(BAR_GROUP + grp, kSoft, dead_row);
+        auto row_max = [&](int r) {
+          const float4 t4 = *reinterpret_cast<const float4*>(part + r * kSoftWarps);
+          return fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
+        };
+        // every thread takes the same decisions from the same shared values
+        const float ml = row_max(lane / kPer);
+        if (ml > ref_lane + (kLazy + kBias)) ref_lane = ml - kBias;  // false for -inf and NaN
+        float alpha[C::NQ];
+        bool resc = false;
 #pragma unroll
-      for (int r = 0; r < C::NQ; ++r) {
-        const float4 t4 = *reinterpret_cast<const float4*>(rm + r * kSoftWarps);
-        const float mt = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
-        const bool need = mt > m_use[r] + kLazy;  // false for -inf and NaN
-        alpha[r] = need ? exp2f(m_use[r] - mt) : 1.f;
-        if (need) m_use[r] = mt;
-        resc |= need;
-      }
-      // every thread took the same decision from the same shared values
-      if (resc) {
-#pragma unroll
-        for (int r = 0; r < C::NQ; ++r) l_part[r] *= alpha[r];
-        if (cur.j > 1) {  // O holds the group's earlier tiles of the segment: rescale it once they are done
+        for (int r = 0; r < C::NQ; ++r) {
+          const float mt = row_max(r);
+          const bool need = mt > ref[r] + (kLazy + kBias);
+          const float to = need ? mt - kBias : ref[r];
+          alpha[r] = need ? exp2f(ref[r] - to) : 1.f;
+          ref[r] = to;
+          l_part[r] *= alpha[r];
+          resc |= need;
+        }
+        if (resc && cur.j > 1) {  // O holds the group's earlier tiles of the segment: rescale it once they are done
           mbar_wait(pv_done + 8 * grp, (u - 1) & 1, failed);
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < C::NB * C::NP; x += 16) {
             // 16 columns: of NQ = 16 rows one term, of fewer rows several
             float o[16];
@@ -890,9 +923,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       float w[C::NQ];
 #pragma unroll
       for (int r = 0; r < C::NQ; ++r) {
-        const float ref = (m_use[r] == kNegInf ? 0.f : m_use[r]) - kBias;
-        w[r] = exp2f(t[r] - ref);
-        l_part[r] += C::KV8 ? exp2f(sc[r] - ref) : w[r];
+        w[r] = exp2f(t[r] - ref[r]);
+        l_part[r] += C::KV8 ? exp2f(sc[r] - ref[r]) : w[r];
       }
 
       // P(i) -> the group's buffer; its last reader, P.V(i - 2), must be done
@@ -900,6 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       if (tq == 0) edge[grp] = clear;
       unsigned char* pbuf = smem + C::OFF_P + grp * C::P_BYTES;
       if constexpr (C::KV8) {
+        // byte pl of row n: 16-byte piece pl / 16, swizzled by n % 8
+        unsigned char* at = pbuf + (pl & 15);
 #pragma unroll
         for (int r = 0; r < C::NQ; r += 2) {
           float2 x = make_float2(w[r], w[r + 1]);
@@ -907,8 +941,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           for (int j = 0; j < 3; ++j) {
             const uint16_t code = next_term(x);
             const int n = j * C::NQ + r;
-            pbuf[swizzled<128>(n, pl >> 4) + (pl & 15)] = static_cast<unsigned char>(code & 0xff);
-            pbuf[swizzled<128>(n + 1, pl >> 4) + (pl & 15)] = static_cast<unsigned char>(code >> 8);
+            at[n * 128 + (((pl >> 4) ^ (n & 7)) << 4)] = static_cast<unsigned char>(code & 0xff);
+            at[(n + 1) * 128 + (((pl >> 4) ^ ((n + 1) & 7)) << 4)] = static_cast<unsigned char>(code >> 8);
           }
         }
       } else {
@@ -929,13 +963,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       // A position that takes no part has weight 0, but its V row may hold
       // anything, NaN too: it is cleared before the MMAs read the slot.
       if (clear) {
+#pragma unroll 1
         for (int p = 0; p < C::NB; ++p) {
           const int slot = (C::seq_v(i, more) + p) % C::RING;
           mbar_wait(v_here + 8 * (grp * C::NB + p), cleared & 1, failed);
           if (dead_row) {
-            for (int ch = 0; ch < C::CH; ++ch)
-              for (int x = 0; x < C::SW; x += 16)
-                *reinterpret_cast<uint4*>(smem + slot * C::SLOT + ch * C::CHUNK + pl * C::SW + x) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int x = 0; x < C::SW * C::CH; x += 16)
+              *reinterpret_cast<uint4*>(smem + slot * C::SLOT + x / C::SW * C::CHUNK + pl * C::SW + x % C::SW) =
+                  make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           mbar_arrive(v_clean + 8 * (grp * C::NB + p));
@@ -945,107 +981,84 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 
       if (cur.j + 2 >= cur.n) {
         // ---- epilogue, after the group's last tile of the segment: its row sums, then this thread's
-        // dim of blocks of dims. Where both groups had tiles they exchange (m, l), and each takes half
-        // of the output from both accumulators.
+        // dim of blocks of dims. Where both groups had tiles they exchange their statistics, and each takes
+        // half of the output from both accumulators. In loops: the code runs once or twice a block, so what
+        // it costs is fetching it (unrolled it took 25,000 cycles).
         const bool both = cur.n > 1;
-        float* rs = reds + 2 * C::NQ * kSoftWarps;
+        const bool direct = cur.begins && cur.ends;
+        const int slot = 2 * c + (cur.begins ? 1 : 0);
         const float lsum = rowreduce<C::NQ>(l_part, lane, AddOp());
-        if (lane % kPer == 0) rs[(lane / kPer) * kSoftWarps + sw] = lsum;
+        if (lane % kPer == 0) {
+          sums[(lane / kPer) * kSoftWarps + sw] = lsum;
+          if (sw == 0) refs[lane / kPer] = ref_lane;
+        }
         named_bar_sync(BAR_GROUP + grp, kSoft);
         mbar_wait(pv_done + 8 * grp, u & 1, failed);
         if (tq < C::NQ) {
-          const float4 t4 = *reinterpret_cast<const float4*>(rs + tq * kSoftWarps);
-          float mr = m_use[0];
-#pragma unroll
-          for (int r = 1; r < C::NQ; ++r)
-            if (r == tq) mr = m_use[r];
-          stat[grp * C::NQ + tq] = make_float2(mr, (t4.x + t4.y) + (t4.z + t4.w));  // fixed order
+          const float4 t4 = *reinterpret_cast<const float4*>(sums + tq * kSoftWarps);
+          stat[grp * C::NQ + tq] = make_float2(refs[tq], (t4.x + t4.y) + (t4.z + t4.w));  // fixed order
         }
         if (both) named_bar_sync(BAR_BOTH, 2 * kSoft);
-        else named_bar_sync(BAR_GROUP + grp, kSoft);
+        if (tq < C::NQ) {
+          float2 s0 = stat[tq], s1 = stat[C::NQ + tq];
+          if (!both && grp == 0) s1 = make_float2(kNone, 0.f);
+          if (!both && grp == 1) s0 = make_float2(kNone, 0.f);
+          const float m = fmaxf(s0.x, s1.x);
+          const float e0 = exp2f(s0.x - m), e1 = exp2f(s1.x - m);
+          const float l = e0 * s0.y + e1 * s1.y;
+          const float by = direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          fac[tq] = e0 * by;
+          fac[C::NQ + tq] = e1 * by;
+          if (!direct && tq < G && (!both || grp == 0))
+            reinterpret_cast<float2*>(a.ws_ml)[static_cast<size_t>(slot) * G + tq] = make_float2(m, l);
+        }
+        named_bar_sync(BAR_GROUP + grp, kSoft);
         tc_fence_after();
-        const bool direct = cur.begins && cur.ends;
-        const int slot = 2 * c + (cur.begins ? 1 : 0);
-#pragma unroll
-        for (int mb = 0; mb < C::NB; ++mb) {
-          if (both && C::NB > 1 && (mb & 1) != grp) continue;
-          // with one block of dims the groups share its rows
-          const int row0 = both && C::NB == 1 ? grp * (C::NQ / 2) : 0;
-          const int row1 = both && C::NB == 1 ? row0 + C::NQ / 2 : C::NQ;
+        // with one block of dims the groups share its rows
+        const int row0 = both && C::NB == 1 ? grp * (C::NQ / 2) : 0;
+        const int row1 = min(G, both && C::NB == 1 ? row0 + C::NQ / 2 : C::NQ);
+#pragma unroll 1
+        for (int mb = both && C::NB > 1 ? grp : 0; mb < C::NB; mb += both && C::NB > 1 ? 2 : 1) {
           float x[C::NQ];
 #pragma unroll
           for (int r = 0; r < C::NQ; ++r) x[r] = 0.f;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {  // the groups' accumulators, in fixed order
-            if (!both && k != grp) continue;
-            float f[C::NQ];
-#pragma unroll
-            for (int r = 0; r < C::NQ; ++r) {
-              const float m0 = stat[r].x, m1 = stat[C::NQ + r].x, m = fmaxf(m0, m1);
-              f[r] = !both ? 1.f : m == kNegInf ? 1.f : exp2f((k ? m1 : m0) - m);
-            }
-            const uint32_t at = o_cols + C::NP * (C::NB * k + mb);
+          // the groups' accumulators, and their terms, in fixed order
+          constexpr int kLoads = C::NQ == 16 ? C::PT : 1;
+#pragma unroll 1
+          for (int n = both ? 0 : grp * kLoads; n < (both ? 2 : grp + 1) * kLoads; ++n) {
+            const int k = n / kLoads, term = n % kLoads;
+            float o[16];
+            tmem_load<16>(o_cols + C::NP * (C::NB * k + mb) + 16 * term, o);
             if constexpr (C::NQ == 16) {
+              const float by = !C::KV8 || term == 0 ? 1.f : term == 1 ? 0.0625f : 0.00390625f;
 #pragma unroll
-              for (int term = 0; term < C::PT; ++term) {
-                float o[16];
-                tmem_load<16>(at + 16 * term, o);
-                const float by = !C::KV8 || term == 0 ? 1.f : term == 1 ? 0.0625f : 0.00390625f;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) x[r] += f[r] * by * o[r];
-              }
+              for (int r = 0; r < 16; ++r) x[r] += fac[k * C::NQ + r] * by * o[r];
             } else {
-              float o[C::NP];
-              tmem_load<C::NP>(at, o);
 #pragma unroll
               for (int r = 0; r < C::NQ; ++r)
-                x[r] += f[r] * (C::KV8 ? o[r] + (o[C::NQ + r] + o[(C::PT - 1) * C::NQ + r] * 0.0625f) * 0.0625f
-                                       : o[r] + o[C::NQ + r]);
+                x[r] += fac[k * C::NQ + r] *
+                        (C::KV8 ? o[r] + (o[C::NQ + r] + o[(C::PT - 1) * C::NQ + r] * 0.0625f) * 0.0625f
+                                : o[r] + o[C::NQ + r]);
             }
           }
           const int d = mb * 128 + pl;  // O^T lanes are head dims
           if (pl < C::DB) {
+            const size_t out0 = (static_cast<size_t>(cur.b) * a.NH + static_cast<size_t>(cur.kvh) * G) * C::HS + d;
+            float* to32 = direct ? (a.out_f32 ? a.out_f32 + out0 : nullptr)
+                                 : a.ws_o + static_cast<size_t>(slot) * G * C::HS + d;
 #pragma unroll
             for (int r = 0; r < C::NQ; ++r) {
-              if (r >= G) break;
-              if (r < row0 || r >= row1) continue;
-              if (direct) {
-                const float2 s0 = stat[(both ? 0 : grp) * C::NQ + r], s1 = stat[C::NQ + r];
-                const float m = fmaxf(s0.x, s1.x);
-                const float L = !both ? s0.y : m == kNegInf ? s0.y + s1.y : exp2f(s0.x - m) * s0.y + exp2f(s1.x - m) * s1.y;
-                const size_t at = (static_cast<size_t>(cur.b) * a.NH + static_cast<size_t>(cur.kvh) * G + r) * C::HS + d;
-                const float y = L == 0.f ? 0.f : x[r] / L;
-                a.out[at] = f32_to_bf16_bits(y);
-                if (a.out_f32) a.out_f32[at] = y;
-              } else {
-                a.ws_o[(static_cast<size_t>(slot) * G + r) * C::HS + d] = x[r];
+              if (r >= row0 && r < row1) {
+                if (direct) a.out[out0 + r * C::HS] = f32_to_bf16_bits(x[r]);
+                if (to32) to32[r * C::HS] = x[r];
               }
             }
           }
-        }
-        if (!direct && tq < G && (!both || grp == 0)) {
-          const float2 s0 = stat[(both ? 0 : grp) * C::NQ + tq], s1 = stat[C::NQ + tq];
-          const float m = fmaxf(s0.x, s1.x);
-          reinterpret_cast<float2*>(a.ws_ml)[static_cast<size_t>(slot) * G + tq] =
-              !both ? s0
-              : m == kNegInf
-                  ? make_float2(m, s0.y + s1.y)
-                  : make_float2(m, exp2f(s0.x - m) * s0.y + exp2f(s1.x - m) * s1.y);
         }
         // the accumulators are free for the next segment (256 arrivals each)
         tc_fence_before();
         mbar_arrive(o_free + 8 * grp);
         mbar_arrive(o_free + 8 * (both ? 1 - grp : grp));
-        if (cur.j + 1 == cur.n && !more && tq == 0) {  // the block's last tile
-          Cut cut{cur.b, cur.kvh, -1, -1};
-          if (!cur.ends) {
-            const Band d = band_of_seq(a, lens, cur.b);
-            const long long u0 = walk.off + static_cast<long long>(cur.kvh) * d.granules;
-            cut.c0 = static_cast<int>(u0 / per);
-            cut.c1 = static_cast<int>((u0 + d.granules - 1) / per);
-          }
-          cuts[c] = cut;
-        }
       }
       more = next_more;
       cur = nxt;
@@ -1100,15 +1113,13 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   auto slot_of = [&](int part) { return 2 * (cut.c0 + part) + (part == 0 ? 1 : 0); };
   const float2* ml = reinterpret_cast<const float2*>(a.ws_ml);
   for (int r = r0 + warp; r <= r1; r += kMergeThreads / 32) {
-    float m = kNegInf;
+    float m = kNegInf;  // every part has a finite reference
     for (int p = lane; p < parts; p += 32) m = fmaxf(m, ml[static_cast<size_t>(slot_of(p)) * G + r].x);
     for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
     float l = 0.f;
     for (int p = lane; p < parts; p += 32) {
       const float2 x = ml[static_cast<size_t>(slot_of(p)) * G + r];
-      // a part whose reference is -inf holds sums that belong to 2^0 (its
-      // weights are 0, or NaN, which has to show)
-      const float f = x.x == kNegInf ? (x.y == 0.f ? 0.f : x.y) : exp2f(x.x - m);
+      const float f = exp2f(x.x - m);
       factor[(r - r0) * parts + p] = f;
       l += f * x.y;
     }
