@@ -6,9 +6,10 @@ Every function here has the name of the C entry point it wraps
 device pointers, the current torch stream becomes the CUDA stream, non-zero
 status codes become FdError. All arithmetic runs in libfd.so's kernels. There
 is no fallback: if libfd.so is missing or a call fails, an exception is raised.
-Where Python headers were available at build time, fd_decode_attn and
-fd_decode_attn_fp8 go through the small compiled module _fdfast (the same
-libfd.so, less host time per call); elsewhere they go through ctypes.
+Where Python headers were available at build time, fd_decode_attn,
+fd_decode_attn_fp8 and the calls of the paged cache go through the small
+compiled module _fdfast (the same libfd.so, less host time per call);
+elsewhere they go through ctypes.
 
 Typical use in a decode loop (every layer its own cache; lens counts the
 current token, whose K/V are already in the cache):
@@ -391,6 +392,16 @@ def decode_attention(q, k_cache, v_cache, lens, window=0, scale=0.0, out=None, s
 # ------------------------------------------------------- the cache in pages
 
 
+def _raw_stream(stream) -> int:
+    """As _stream; the current stream without an object made for it, where torch offers that."""
+    if stream is not None:
+        return _stream(stream) or 0
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(torch.cuda.current_device()) if get else _stream(None) or 0
+
+
+
 def fd_paged_plan(B, NH, NKV, HS, page_size, max_pages, window, device=None, kv_dtype=FD_KV_BF16) -> fd_paged_plan_t:
     if device is None:
         import torch
@@ -410,26 +421,45 @@ def fd_paged_plan_sms(B, NH, NKV, HS, page_size, max_pages, window, num_sms, kv_
 
 def fd_paged_attn(q, k_pages, v_pages, k_scale, v_scale, out, table, lens, B, NH, NKV, HS, page_size, num_pages,
                   max_pages, window, scale, kv_dtype, stream=None) -> None:
-    _check(load_library().fd_paged_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-                                        _ptr(out), _ptr(table), _ptr(lens), B, NH, NKV, HS, page_size, num_pages,
-                                        max_pages, window, float(scale), kv_dtype, _stream(stream)), "fd_paged_attn")
+    f = _fast()
+    if f is not None:
+        rc = f.paged_attn(q, k_pages, v_pages, k_scale, v_scale, out, table, lens, B, NH, NKV, HS, page_size,
+                          num_pages, max_pages, window, scale, kv_dtype, _raw_stream(stream))
+    else:
+        rc = load_library().fd_paged_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                                          _ptr(out), _ptr(table), _ptr(lens), B, NH, NKV, HS, page_size, num_pages,
+                                          max_pages, window, scale, kv_dtype, _stream(stream))
+    _check(rc, "fd_paged_attn")
 
 
 def fd_paged_attn_ex(plan: fd_paged_plan_t, workspace, workspace_bytes, out_f32, q, k_pages, v_pages, k_scale, v_scale,
                      out, table, lens, B, NH, NKV, HS, page_size, num_pages, max_pages, window, scale,
                      stream=None) -> None:
-    _check(load_library().fd_paged_attn_ex(ctypes.byref(plan), _ptr(workspace), int(workspace_bytes), _ptr(out_f32),
-                                           _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-                                           _ptr(out), _ptr(table), _ptr(lens), B, NH, NKV, HS, page_size, num_pages,
-                                           max_pages, window, float(scale), _stream(stream)), "fd_paged_attn_ex")
+    f = _fast()
+    if f is not None:
+        rc = f.paged_attn_ex(ctypes.addressof(plan), workspace, workspace_bytes, out_f32, q, k_pages, v_pages, k_scale,
+                             v_scale, out, table, lens, B, NH, NKV, HS, page_size, num_pages, max_pages, window, scale,
+                             _raw_stream(stream))
+    else:
+        rc = load_library().fd_paged_attn_ex(ctypes.byref(plan), _ptr(workspace), workspace_bytes, _ptr(out_f32),
+                                             _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                                             _ptr(out), _ptr(table), _ptr(lens), B, NH, NKV, HS, page_size, num_pages,
+                                             max_pages, window, scale, _stream(stream))
+    _check(rc, "fd_paged_attn_ex")
 
 
 def fd_paged_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, table, lens, start, count, B, T, NKV, HS,
                     page_size, num_pages, max_pages, k_stride, v_stride, kv_dtype, stream=None) -> None:
-    _check(load_library().fd_paged_append(_ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-                                          _ptr(v_scale), _ptr(table), _ptr(lens), _ptr(start), _ptr(count), B, T, NKV,
-                                          HS, page_size, num_pages, max_pages, int(k_stride), int(v_stride), kv_dtype,
-                                          _stream(stream)), "fd_paged_append")
+    f = _fast()
+    if f is not None:
+        rc = f.paged_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, table, lens, start, count, B, T, NKV,
+                            HS, page_size, num_pages, max_pages, k_stride, v_stride, kv_dtype, _raw_stream(stream))
+    else:
+        rc = load_library().fd_paged_append(_ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                                            _ptr(v_scale), _ptr(table), _ptr(lens), _ptr(start), _ptr(count), B, T,
+                                            NKV, HS, page_size, num_pages, max_pages, k_stride, v_stride, kv_dtype,
+                                            _stream(stream))
+    _check(rc, "fd_paged_append")
 
 
 def fd_pages_workspace_bytes(B, num_pages) -> int:
@@ -438,32 +468,59 @@ def fd_pages_workspace_bytes(B, num_pages) -> int:
 
 def fd_pages_reserve(table, lens, refs, grow, granted, moves, workspace, workspace_bytes, B, max_pages, num_pages,
                      page_size, stream=None) -> None:
-    _check(load_library().fd_pages_reserve(_ptr(table), _ptr(lens), _ptr(refs), _ptr(grow), _ptr(granted),
-                                           _ptr(moves), _ptr(workspace), int(workspace_bytes), B, max_pages,
-                                           num_pages, page_size, _stream(stream)), "fd_pages_reserve")
+    f = _fast()
+    if f is not None:
+        rc = f.pages_reserve(table, lens, refs, grow, granted, moves, workspace, workspace_bytes, B, max_pages,
+                             num_pages, page_size, _raw_stream(stream))
+    else:
+        rc = load_library().fd_pages_reserve(_ptr(table), _ptr(lens), _ptr(refs), _ptr(grow), _ptr(granted),
+                                             _ptr(moves), _ptr(workspace), workspace_bytes, B, max_pages, num_pages,
+                                             page_size, _stream(stream))
+    _check(rc, "fd_pages_reserve")
 
 
 def fd_pages_fork(table, lens, parent, table_out, lens_out, refs, B, B_out, max_pages, num_pages, stream=None) -> None:
-    _check(load_library().fd_pages_fork(_ptr(table), _ptr(lens), _ptr(parent), _ptr(table_out), _ptr(lens_out),
-                                        _ptr(refs), B, B_out, max_pages, num_pages, _stream(stream)), "fd_pages_fork")
+    f = _fast()
+    if f is not None:
+        rc = f.pages_fork(table, lens, parent, table_out, lens_out, refs, B, B_out, max_pages, num_pages,
+                          _raw_stream(stream))
+    else:
+        rc = load_library().fd_pages_fork(_ptr(table), _ptr(lens), _ptr(parent), _ptr(table_out), _ptr(lens_out),
+                                          _ptr(refs), B, B_out, max_pages, num_pages, _stream(stream))
+    _check(rc, "fd_pages_fork")
 
 
 def fd_pages_free(table, lens, refs, keep, window, B, max_pages, num_pages, page_size, stream=None) -> None:
-    _check(load_library().fd_pages_free(_ptr(table), _ptr(lens), _ptr(refs), _ptr(keep), window, B, max_pages,
-                                        num_pages, page_size, _stream(stream)), "fd_pages_free")
+    f = _fast()
+    if f is not None:
+        rc = f.pages_free(table, lens, refs, keep, window, B, max_pages, num_pages, page_size, _raw_stream(stream))
+    else:
+        rc = load_library().fd_pages_free(_ptr(table), _ptr(lens), _ptr(refs), _ptr(keep), window, B, max_pages,
+                                          num_pages, page_size, _stream(stream))
+    _check(rc, "fd_pages_free")
 
 
 def fd_pages_compact(table, refs, moves, workspace, workspace_bytes, B, max_pages, num_pages, stream=None) -> None:
-    _check(load_library().fd_pages_compact(_ptr(table), _ptr(refs), _ptr(moves), _ptr(workspace),
-                                           int(workspace_bytes), B, max_pages, num_pages, _stream(stream)),
-           "fd_pages_compact")
+    f = _fast()
+    if f is not None:
+        rc = f.pages_compact(table, refs, moves, workspace, workspace_bytes, B, max_pages, num_pages,
+                             _raw_stream(stream))
+    else:
+        rc = load_library().fd_pages_compact(_ptr(table), _ptr(refs), _ptr(moves), _ptr(workspace), workspace_bytes,
+                                             B, max_pages, num_pages, _stream(stream))
+    _check(rc, "fd_pages_compact")
 
 
 def fd_pages_copy(k_pages, v_pages, k_scale, v_scale, moves, room, layers, num_pages, NKV, page_size, HS, kv_dtype,
                   stream=None) -> None:
-    _check(load_library().fd_pages_copy(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(moves), room,
-                                        layers, num_pages, NKV, page_size, HS, kv_dtype, _stream(stream)),
-           "fd_pages_copy")
+    f = _fast()
+    if f is not None:
+        rc = f.pages_copy(k_pages, v_pages, k_scale, v_scale, moves, room, layers, num_pages, NKV, page_size, HS,
+                          kv_dtype, _raw_stream(stream))
+    else:
+        rc = load_library().fd_pages_copy(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(moves),
+                                          room, layers, num_pages, NKV, page_size, HS, kv_dtype, _stream(stream))
+    _check(rc, "fd_pages_copy")
 
 
 def paged_attention(q, k_pages, v_pages, table, lens, window=0, scale=0.0, k_scale=None, v_scale=None, out=None,

@@ -73,28 +73,28 @@ __device__ __forceinline__ long long first_unit(const AppendArgs& a, int b) {
   return static_cast<long long>(max(a.start[b], 0) / a.P) + 2ll * b;
 }
 
-__device__ __forceinline__ Segment find_segment(const AppendArgs& a, long long unit, bool report) {
-  if (!a.start) return segment_of(a, static_cast<int>(unit), 0, report);
-  int lo = 0, hi = a.B;  // the last b with first_unit(b) <= unit
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first_unit(a, mid) <= unit) lo = mid;
-    else hi = mid;
+// The last b in [0, B) with first_unit(b) <= unit, found by the whole warp: each
+// round tests 32 places at once, so 1024 sequences take two loads.
+__device__ __forceinline__ int sequence_of(const AppendArgs& a, long long unit, int lane) {
+  int lo = 0, n = a.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int b = lo + lane * step;
+    const bool in = lane * step < n && first_unit(a, b) <= unit;
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    const int at = m ? 31 - __clz(m) : 0;
+    n = min(step, n - at * step);
+    lo += at * step;
   }
-  const long long seg = unit - first_unit(a, lo);
-  if (seg < 0 || seg > 0x3fffffff) return Segment{lo, 0, 0, 0, -1};
-  return segment_of(a, lo, static_cast<int>(seg), report);
+  return lo;
 }
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(__half(h));
-}
-
-// Nearest E4M3 code of x / s: NaN where x is not finite, 0 where s is 0.
-__device__ __forceinline__ uint8_t quantise(float x, float s) {
-  const float y = isfinite(x) ? (s > 0.f ? x / s : 0.f) : __int_as_float(0x7fffffff);
-  return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ Segment find_segment(const AppendArgs& a, long long unit, int lane, bool report) {
+  if (!a.start) return segment_of(a, static_cast<int>(unit), 0, report);
+  const int b = sequence_of(a, unit, lane);
+  const long long seg = unit - first_unit(a, b);
+  if (seg < 0 || seg > 0x3fffffff) return Segment{b, 0, 0, 0, -1};
+  return segment_of(a, b, static_cast<int>(seg), report);
 }
 
 // Least power of two s with amax <= 448 s, at least 2^-126; 0 for amax = 0.
@@ -106,49 +106,116 @@ __device__ __forceinline__ float block_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
 }
 
-constexpr int kAppendThreads = 128;
+// Codes of x / s. A power of two (every scale that this writer makes) divides
+// exactly by a product with its reciprocal.
+struct Divisor {
+  float s, inv;
+  bool pow2;
+  __device__ explicit Divisor(float scale) : s(scale) {
+    const uint32_t u = __float_as_uint(scale);
+    pow2 = (u & 0x7fffffu) == 0 && u >= 0x00800000u && u < 0x7e800000u;  // 2^-126 .. 2^125
+    inv = pow2 ? __uint_as_float(0x7f000000u - u) : 0.f;
+  }
+  __device__ float operator()(float x) const { return pow2 ? x * inv : (s > 0.f ? x / s : 0.f); }
+};
 
-// One block per (unit, head, K or V).
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
-  __shared__ float red[kAppendThreads / 32];
-  const int head = blockIdx.y, w = blockIdx.z, tid = threadIdx.x;
-  const Segment g = find_segment(a, blockIdx.x, head == 0 && w == 0 && tid == 0);
+__device__ __forceinline__ uint16_t quantise2(float x, float y) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float finite_or_nan(float x) { return isfinite(x) ? x : __int_as_float(0x7fffffff); }
+
+// 8 bf16 values -> 8 codes.
+__device__ __forceinline__ uint2 quantise8(const uint4& v, const Divisor& by) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = quantise2(by(finite_or_nan(__uint_as_float(u[i] << 16))), by(finite_or_nan(__uint_as_float(u[i] & 0xffff0000u))));
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// The codes of four values, multiplied.
+__device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
+  const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(c & 0xffff), __NV_E4M3)));
+  const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(c >> 16), __NV_E4M3)));
+  return quantise2(a.x * ratio, a.y * ratio) | (static_cast<uint32_t>(quantise2(b.x * ratio, b.y * ratio)) << 16);
+}
+
+// An item - one head's K or V of a unit - belongs to WPI warps, each thread of
+// which holds VPT vectors of 8 elements in registers: the block's largest value
+// has to be known before the first code is written, and the tokens are read
+// once. A block looks its unit up once for BLOCK / (32 WPI) items.
+// Bound by memory: 2 bytes in and 1 out an element.
+template <bool KV8, int VPT, int WPI>
+__global__ void __launch_bounds__(WPI > 8 ? WPI * 32 : 256) append_kernel(const AppendArgs a) {
+  constexpr int kBlock = WPI > 8 ? WPI * 32 : 256;
+  constexpr int kItems = kBlock / 32 / WPI;
+  __shared__ uint32_t red[kBlock / 32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const Segment g = find_segment(a, blockIdx.x, lane, blockIdx.y == 0 && tid == 0);
   if (g.n <= 0) return;
+  const int item = blockIdx.y * kItems + tid / (32 * WPI);
+  const bool there = item < 2 * a.NKV;
+  const int w = item & 1, head = item >> 1, t = tid % (32 * WPI);
+  const int row_shift = 28 - __clz(a.HS);  // vectors of a row: HS / 8
+  const int vecs = there ? g.n << row_shift : 0;
+  const long long stride = w ? a.stride[1] : a.stride[0];
+  const uint16_t* x = (w ? a.x[1] : a.x[0]) + g.row * stride + static_cast<size_t>(head) * a.HS;
+  uint4 v[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int at = t + i * 32 * WPI, row = at >> row_shift, col = at & ((1 << row_shift) - 1);
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (at < vecs) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + row * stride + col * 8));
+  }
   const size_t block = static_cast<size_t>(g.page) * a.NKV + head;
   const size_t base = (block * a.P + g.slot) * a.HS;
-  const int rowv = a.HS / 8;  // vectors of 8 elements in a row
-  const uint16_t* x = a.x[w] + static_cast<long long>(g.row) * a.stride[w] + static_cast<size_t>(head) * a.HS;
-  if (!a.kv8) {
-    uint16_t* to = static_cast<uint16_t*>(a.pages[w]) + base;
-    for (int i = tid; i < g.n * rowv; i += kAppendThreads)
-      reinterpret_cast<uint4*>(to)[i] =
-          *reinterpret_cast<const uint4*>(x + static_cast<long long>(i / rowv) * a.stride[w] + (i % rowv) * 8);
-    return;
-  }
-  float amax = 0.f;
-  for (int i = tid; i < g.n * rowv; i += kAppendThreads) {
-    const uint16_t* at = x + static_cast<long long>(i / rowv) * a.stride[w] + (i % rowv) * 8;
-    for (int k = 0; k < 8; ++k) {
-      const float f = fabsf(bf16_bits_to_f32(at[k]));
-      if (isfinite(f)) amax = fmaxf(amax, f);
+  if constexpr (!KV8) {
+    uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(w ? a.pages[1] : a.pages[0]) + base);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = v[i];
+  } else {
+    float* scale = (w ? a.scale[1] : a.scale[0]) + block;
+    const float old = there && g.slot > 0 ? *scale : 0.f;
+    // the largest |x| by its bits, two at a time; not finite ones only count as 0
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t abs2 = u[k] & 0x7fff7fffu;
+        m = __vmaxu2(m, abs2 & ~__vcmpgeu2(abs2, 0x7f807f80u));
+      }
     }
+    m = max(m & 0xffffu, m >> 16);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if constexpr (WPI > 1) {
+      if (lane == 0) red[tid >> 5] = m;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < WPI; ++i) m = max(m, red[tid / (32 * WPI) * WPI + i]);
+    }
+    if (!there) return;
+    const float s = fmaxf(block_scale(__uint_as_float(m << 16)), old);
+    uint8_t* pages = static_cast<uint8_t*>(w ? a.pages[1] : a.pages[0]);
+    if (g.slot > 0 && s > old) {  // the earlier tokens' codes, rounded to the new scale
+      const float ratio = old / s;
+      uint4* held = reinterpret_cast<uint4*>(pages + block * a.P * a.HS);
+      for (int i = t; i < g.slot * a.HS / 16; i += 32 * WPI) {
+        const uint4 c = held[i];
+        held[i] = make_uint4(rescale4(c.x, ratio), rescale4(c.y, ratio), rescale4(c.z, ratio), rescale4(c.w, ratio));
+      }
+    }
+    const Divisor by(s);
+    uint2* to = reinterpret_cast<uint2*>(pages + base);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = quantise8(v[i], by);
+    if (t == 0) *scale = s;
   }
-  for (int i = 16; i; i >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, i));
-  if ((tid & 31) == 0) red[tid >> 5] = amax;
-  const float old = g.slot > 0 ? a.scale[w][block] : 0.f;
-  __syncthreads();
-  for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, red[i]);
-  const float s = fmaxf(block_scale(amax), old);
-  uint8_t* pages = static_cast<uint8_t*>(a.pages[w]);
-  if (g.slot > 0 && s > old) {
-    const float ratio = old / s;
-    uint8_t* held = pages + block * a.P * a.HS;
-    for (int i = tid; i < g.slot * a.HS; i += kAppendThreads) held[i] = quantise(e4m3_to_f32(held[i]) * ratio, 1.f);
-  }
-  uint8_t* to = pages + base;
-  for (int i = tid; i < g.n * a.HS; i += kAppendThreads)
-    to[i] = quantise(bf16_bits_to_f32(x[static_cast<long long>(i / a.HS) * a.stride[w] + i % a.HS]), s);
-  if (tid == 0) a.scale[w][block] = s;
 }
 
 // ================================================================ bookkeeping
@@ -487,12 +554,35 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 int row_blocks(int max_pages) { return std::min((max_pages + kTableThreads - 1) / kTableThreads, 64); }
 
+template <bool KV8, int VPT, int WPI>
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
+  constexpr int kBlock = WPI > 8 ? WPI * 32 : 256, kItems = kBlock / 32 / WPI;
+  const long long units = a.start ? static_cast<long long>(a.T) / a.P + 2ll * a.B : a.B;
+  append_kernel<KV8, VPT, WPI>
+      <<<dim3(static_cast<unsigned>(units), (2 * a.NKV + kItems - 1) / kItems), kBlock, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// Warps of an item: as many as hold a page's tokens of one head in 8 vectors a
+// thread (4 where that is less than a warp's 8). Without `start` an item is one token.
+template <bool KV8>
+cudaError_t launch_append_type(const AppendArgs& a, cudaStream_t stream) {
+  if (!a.start) return launch_append<KV8, 2, 1>(a, stream);
+  switch (a.P * a.HS / 2048) {
+    case 0: return launch_append<KV8, 4, 1>(a, stream);
+    case 1: return launch_append<KV8, 8, 1>(a, stream);
+    case 2: return launch_append<KV8, 8, 2>(a, stream);
+    case 4: return launch_append<KV8, 8, 4>(a, stream);
+    case 8: return launch_append<KV8, 8, 8>(a, stream);
+    case 16: return launch_append<KV8, 8, 16>(a, stream);
+    default: return launch_append<KV8, 8, 32>(a, stream);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t stream) {
-  const long long units = a.start ? static_cast<long long>(a.T) / a.P + 2ll * a.B : a.B;
-  append_kernel<<<dim3(static_cast<unsigned>(units), a.NKV, 2), kAppendThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return a.kv8 ? launch_append_type<true>(a, stream) : launch_append_type<false>(a, stream);
 }
 
 cudaError_t launch_pages_reserve(int* table, int* lens, int* refs, const int* grow, int* granted, int* moves, int* ws,
