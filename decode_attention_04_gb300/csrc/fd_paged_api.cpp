@@ -1,6 +1,7 @@
 // Host side of the paged cache: argument checks, the plan, the library-owned
 // workspace, and the exported C entry points declared in fd_paged_attn.h.
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -54,7 +55,11 @@ int make_plan(int B, int NH, int NKV, int HS, int page_size, int max_pages, int 
   fd_paged_plan_t p{};
   p.blocks = num_sms;
   p.granule = 32;
-  p.min_share = 1;
+  // At least 64 KB of K and V a share: below that a merge of its partial costs
+  // more than the SMs left idle (256 positions of 8 heads of 128, E4M3, in
+  // shares of 8 KB 9.8 us, of 32 KB 9.2, of 64 KB, whole bands, 7.6; 1024
+  // positions of 8 heads of 256 in 32 KB 10.9, 64 KB 10.5, 128 KB 11.1).
+  p.min_share = std::max(1, (64 << 10) / (2 * p.granule * HS * (kv_dtype == FD_KV_E4M3 ? 1 : 2)));
   p.num_sms = num_sms;
   p.kv_dtype = kv_dtype;
   p.workspace_bytes = ws_bytes(p.blocks, NH / NKV, HS);

@@ -10,20 +10,22 @@
 // is written to the output directly.
 //
 // A block, per tile of 128 positions (a share's part of one band is a segment):
-//   * Warps 0 (K) and 11 (V) fill a ring of shared-memory slots (one slot: the
+//   * Two warps each for K and V fill rings of shared-memory slots (one slot: the
 //     tile's 128 positions x 128 head dims) by TMA, a box of one page's rows
-//     (32 at most) and 128 bytes each; lane i looks up and copies box i. The ring's order
-//     is K(0), then K(i + 1), V(i): the scores of the next tile are computed while
-//     the softmax of this one runs. A warp spends about 200 cycles on a slot and
-//     70 on each box, so one warp could not fill 16 KB slots at the rate of HBM.
-//   * Warp 1 issues the MMAs in the ring's order, accumulators in tensor
-//     memory: S^T (positions x query rows) = K Q^T and O^T (dims x query rows)
-//     += V^T P^T. With K as the 128-row operand the tensor cores read every code
-//     once, as it lies in the cache: nothing is widened.
-//   * Warps 2-5 and 6-9, two groups, turn scores into weights, a position a
+//     (32 at most) and 128 bytes each; a lane looks up and copies a box. A box
+//     costs its warp about 70 cycles, a slot 200 more: one warp for both tensors
+//     fell short of the rate of HBM with pages of 16 (ragged batch 161 us, a warp
+//     each 117).
+//   * One warp issues S^T (positions x query rows) = K Q^T, one O^T (dims x
+//     query rows) += V^T P^T, accumulators in tensor memory. With K as the 128-row operand the
+//     tensor cores read every code once, as it lies in the cache: nothing is
+//     widened. A warp for both products was the bottleneck: a wait that finds
+//     its barrier complete takes 100 cycles, the MMAs of a tile less.
+//   * Two groups of four warps turn scores into weights, a position a
 //     thread: the groups take the tiles in turn, each with an accumulator, a running
 //     maximum and sums of its own, which are joined at the segment's end.
-//   * Warp 10 brings the query rows of the next segments.
+//   * One warp brings the query rows of the next segments.
+//   The softmax groups take registers over from the other warps.
 //
 // E4M3 products are exact but for the other operand, which enters as a sum of
 // E4M3 terms, each in MMA columns of its own, term i scaled by 16^i so that it
@@ -196,11 +198,37 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// Waits for a barrier of each active lane (bounded, as mbar_wait): one round
+// trip for all of them.
+__device__ __forceinline__ void wait_lanes(uint32_t bar, uint32_t parity, bool active, bool& failed) {
+  if (active) mbar_wait(bar, parity, failed);
+  failed = __any_sync(0xffffffffu, failed);
+  __syncwarp();
+}
+
+// A wait of a whole warp. Lanes leave mbar_wait one by one: a lane that ran
+// ahead could let the barrier pass two phases before the last one looked, which
+// then would wait for ever; and tcgen05.ld wants the warp in step.
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, bool& failed) {
+  mbar_wait(bar, parity, failed);
+  __syncwarp();
+}
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ------------------------------------------------------------- the division of work
 
 constexpr int kTile = 128;      // positions per tile: the M of the score MMA
 constexpr int kGranule = 32;    // positions
 constexpr int kLenCache = 1024; // lengths kept in shared memory when there are no more sequences
+constexpr int kWarpSeqs = 128;  // a warp finds its share by itself when there are no more sequences
 
 struct Band {
   unsigned lo;
@@ -281,11 +309,15 @@ __device__ __forceinline__ void next_tile(const PagedArgs& a, const int* cache, 
 
 constexpr int kSoftWarps = 4;  // of a softmax group: one TMEM lane quarter each
 constexpr int kSoft = kSoftWarps * 32;
-constexpr int W_K = 0, W_MMA = 1, W_SOFT0 = 2, W_Q = W_SOFT0 + 2 * kSoftWarps, W_V = W_Q + 1;
-constexpr int kThreads = (W_V + 1) * 32;
+// Warps, by fours (warpgroups): the first copy warps and the MMA warps; the two
+// softmax groups; the query rows and the second copy warps.
+constexpr int W_K = 0, W_QK = 1, W_PV = 2, W_V = 3, W_SOFT0 = 4, W_Q = 12, W_K2 = 13, W_V2 = 14;
+constexpr int kThreads = 16 * 32;
+// Registers a thread of each warpgroup: 72 + 2 * 184 + 64 <= 4 * 128, what the block is launched with.
+constexpr int kRegsIssue = 72, kRegsSoft = 184, kRegsHelp = 64;
+static_assert(kRegsIssue + 2 * kRegsSoft + kRegsHelp <= 4 * (65536 / kThreads), "registers of the launch");
 constexpr int kQRing = 8;      // segments whose query multipliers are kept
-// named barriers
-constexpr int BAR_GROUP = 1, BAR_TMEM = 3, BAR_BOTH = 4;
+constexpr int BAR_GROUP = 1, BAR_BOTH = 3;  // named barriers: of a softmax group (two), of both
 
 constexpr int round16(int x) { return (x + 15) / 16 * 16; }
 constexpr int pow2_cols(int x) { return x <= 32 ? 32 : x <= 64 ? 64 : x <= 128 ? 128 : x <= 256 ? 256 : 512; }
@@ -321,18 +353,16 @@ struct Cfg {
   static constexpr int OFF_QMUL = OFF_RED + RED_BYTES;  // f32 [kQRing][16]
   static constexpr int OFF_LEN = OFF_QMUL + kQRing * 16 * 4;
   static constexpr int OFF_BAR = OFF_LEN + kLenCache * 4;
-  // full[RING], empty[RING], s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], q_free[2], o_free[2], mma_done,
+  // full[RING], empty[RING], s_full[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], q_free[2], o_free[2], mma_done[2],
   // v_clean[2][NB], v_here[2][NB]; the pairs by the parity of a tile (its group) or, for q, of a segment
-  static constexpr int NBAR = 2 * RING + 15 + 4 * NB;
+  static constexpr int NBAR = 2 * RING + 16 + 4 * NB;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tensor memory address; share; edge[2]
   static constexpr int SMEM = OFF_MISC + 64 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(P_BYTES % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms are aligned");
   static_assert(OFF_BAR % 8 == 0, "barriers");
-  static_assert(RING >= 4, "two slots of each of K and V");
-  // Stream position of the first slot of tile t's K and V: K(0), then K(t + 1), V(t).
-  static __device__ __forceinline__ int seq_k(int t) { return t == 0 ? 0 : NB * (2 * t - 1); }
-  static __device__ __forceinline__ int seq_v(int t, bool more) { return NB * (2 * t + (more ? 2 : 1)); }
+  static constexpr int RK = RING / 2, RV = RING - RK;  // K's slots, then V's
+  static_assert(RK >= 2, "two slots of each of K and V");
   // Instruction descriptor: D f32; A and B E4M3 (0) or bf16 (1 in bits 7 and
   // 10); bit 15: A is MN-major; N / 8 at 17, M / 16 at 24.
   static constexpr uint32_t IDESC_QK = (1u << 4) | (KV8 ? 0u : (1u << 7) | (1u << 10)) |
@@ -418,19 +448,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   const uint32_t full = bar0, empty = full + 8 * C::RING;
   const uint32_t s_full = empty + 8 * C::RING, s_free = s_full + 16, p_ready = s_free + 16, pv_done = p_ready + 16;
   const uint32_t q_ready = pv_done + 16, q_free = q_ready + 16, o_free = q_free + 16, mma_done = o_free + 16;
-  const uint32_t v_clean = mma_done + 8, v_here = v_clean + 16 * C::NB;
+  const uint32_t v_clean = mma_done + 16, v_here = v_clean + 16 * C::NB;
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
   float* qmul = reinterpret_cast<float*>(smem + C::OFF_QMUL);
   int* lens = reinterpret_cast<int*>(smem + C::OFF_LEN);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
-  long long* share = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);  // granules: per share, all; before the first band
-  int* share_at = reinterpret_cast<int*>(smem + C::OFF_MISC + 40);  // where the share begins: sequence, head, granule
-  volatile int* edge = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 52);  // of tile i: V has rows to clear
+  int* share_at = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // where the share begins: sequence, head, granule
+  volatile int* edge = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 32);  // of tile i: V has rows to clear
 
   // Set-up that reads no input, overlapping the previous kernel's tail.
   if (tid == 0) {
     for (int k = 0; k < C::RING; ++k) {
-      mbar_init(full + 8 * k, 1);
+      mbar_init(full + 8 * k, 2);  // both copy warps, and the bytes
       mbar_init(empty + 8 * k, 1);
     }
     for (int j = 0; j < 2; ++j) {
@@ -447,15 +476,93 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_init(v_here + 8 * j, 1);
     }
     mbar_init(mma_done, 1);
+    mbar_init(mma_done + 8, 1);
     fence_mbar_init();
     prefetch_tensor_map(&maps.k);
     prefetch_tensor_map(&maps.v);
   }
+  if (warp == W_QK) {
+    tmem_alloc(base + C::OFF_MISC, C::COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // The total of granules, then the sequence in which this block's share begins.
-  {
+  // This block's share of the granules, and where it begins.
+  long long per, total;
+  Walk walk;
+  walk.t.ok = false;
+  walk.t.seg = -1;
+  walk.t.j = walk.t.n = 0;
+  walk.t.b = walk.kvh = walk.g0 = 0;
+  auto shares = [&](long long heads_granules) {  // granules of one head of every sequence
+    total = heads_granules * a.NKV;
+    per = total <= 0x7fff0000ll ? static_cast<int>(total + a.blocks - 1) / a.blocks : (total + a.blocks - 1) / a.blocks;
+    per = max(per, static_cast<long long>(a.min_share));
+    walk.left = min(per, total - per * c);
+  };
+  // sequence b, whose bands have x granules each and begin at granule off of the stream, holds the share's first
+  auto begin_at = [&](int b, long long off, int x) {
+    const long long in = per * c - off;
+    walk.t.b = b;
+    if (in <= 0x7fffffffll) {
+      walk.kvh = static_cast<int>(in) / x;
+      walk.g0 = static_cast<int>(in) % x;
+    } else {
+      walk.kvh = static_cast<int>(in / x);
+      walk.g0 = static_cast<int>(in % x);
+    }
+  };
+  if (a.B <= kWarpSeqs) {
+    // every warp by itself, without a barrier: a lane takes four sequences
+    int x[4], before[4];
+    long long mine = 0;  // 2^26 granules at most in each
+    unsigned flags = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int b = 4 * lane + k;
+      const int raw_len = b < a.B ? a.lens[b] : 0, len = clamp_len(a, raw_len);
+      if (raw_len < 0) flags |= FD_DEVERR_LEN_NEGATIVE;
+      if (raw_len > len) flags |= FD_DEVERR_LEN_CLAMPED;
+      if (b < a.B) lens[b] = len;  // each warp writes the same, and reads its own
+      x[k] = band_from(a, len).granules;
+      before[k] = static_cast<int>(mine);
+      mine += x[k];
+    }
+    if (c == 0 && warp == 0 && flags) atomicOr(&g_device_error, flags);
+    long long upto = mine;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, i);
+      if (lane >= i) upto += y;
+    }
+    shares(__shfl_sync(0xffffffffu, upto, 31));
+    int found = -1;
+    long long off = 0;
+    int gran = 1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const long long o = (upto - mine + before[k]) * a.NKV;
+      if (x[k] > 0 && o <= per * c && per * c < o + static_cast<long long>(x[k]) * a.NKV) {
+        found = 4 * lane + k;
+        off = o;
+        gran = x[k];
+      }
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, found >= 0);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      found = __shfl_sync(0xffffffffu, found, src);
+      off = __shfl_sync(0xffffffffu, off, src);
+      gran = __shfl_sync(0xffffffffu, gran, src);
+      begin_at(found, off, gran);
+    }
+    __syncwarp();
+  } else {
     long long* sums = reinterpret_cast<long long*>(smem + C::OFF_RED);  // [kThreads / 32]
     long long mine = 0;
     unsigned flags = 0;
@@ -467,23 +574,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mine += band_from(a, len).granules;
     }
     if (c == 0 && flags) atomicOr(&g_device_error, flags);
-    long long s = mine;
-    for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-    if (lane == 0) sums[warp] = s;
+    for (int i = 16; i; i >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, i);
+    if (lane == 0) sums[warp] = mine;
     __syncthreads();
-    long long total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) total += sums[i];
-    total *= a.NKV;
-    const long long per = max((total + a.blocks - 1) / a.blocks, static_cast<long long>(a.min_share));
+    long long all = 0;
+    for (int i = 0; i < kThreads / 32; ++i) all += sums[i];
+    shares(all);
     const long long start = per * c;
-    if (tid == 0) {
-      share[0] = per;
-      share[1] = total;
-    }
     long long before = 0;  // granules (of one head) of the sequences before this chunk
     for (int b0 = 0; b0 < a.B && start < total; b0 += kThreads) {
       const int b = b0 + tid;
-      const long long x = b < a.B ? band_of_seq(a, lens, b).granules : 0;
+      const int x = b < a.B ? band_of_seq(a, lens, b).granules : 0;
       long long inc = x;
       for (int i = 1; i < 32; i <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, inc, i);
@@ -492,68 +593,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       __syncthreads();
       if (lane == 31) sums[warp] = inc;
       __syncthreads();
-      long long all = 0;
+      all = 0;
       for (int i = 0; i < kThreads / 32; ++i) {
         if (i < warp) inc += sums[i];
         all += sums[i];
       }
       const long long off = (before + inc - x) * a.NKV;
-      if (x > 0 && off <= start && start < off + x * a.NKV) {
-        share[2] = off;
-        share_at[0] = b;
-        share_at[1] = static_cast<int>((start - off) / x);
-        share_at[2] = static_cast<int>((start - off) % x);
+      if (x > 0 && off <= start && start < off + static_cast<long long>(x) * a.NKV) {
+        begin_at(b, off, x);
+        share_at[0] = walk.t.b;
+        share_at[1] = walk.kvh;
+        share_at[2] = walk.g0;
       }
       before += all;
       if (start < before * a.NKV) break;
     }
     __syncthreads();
+    if (walk.left > 0) {
+      walk.t.b = share_at[0];
+      walk.kvh = share_at[1];
+      walk.g0 = share_at[2];
+    }
   }
-  const long long per = share[0], total = share[1];
-  Walk walk;
-  walk.left = min(per, total - per * c);
-  walk.t.ok = false;
-  walk.t.seg = -1;
-  walk.t.j = walk.t.n = 0;
   const bool work = walk.left > 0;
   if (work) {
-    walk.t.b = share_at[0];
-    walk.kvh = share_at[1];
-    walk.g0 = share_at[2];
     walk.d = band_of_seq(a, lens, walk.t.b);
     next_tile(a, lens, walk);
   }
 
-  // Rows of empty sequences are zero.
-  for (int b = c; b < a.B; b += gridDim.x) {
-    if ((a.B <= kLenCache ? lens[b] : clamp_len(a, a.lens[b])) > 0) continue;
-    for (int i = tid; i < a.NH * C::HS; i += kThreads) {
-      const size_t o = static_cast<size_t>(b) * a.NH * C::HS + i;
-      a.out[o] = 0;
-      if (a.out_f32) a.out_f32[o] = 0.f;
-    }
-  }
   Cut* cuts = reinterpret_cast<Cut*>(a.cuts);
-  if (!work) {
-    if (tid == 0) cuts[c].c0 = -1;
-    return;
-  }
+  if (!work && tid == 0) cuts[c].c0 = -1;
 
   bool failed = false;
-  int slots_used = 0;  // of the ring's order, by K and V (the copy warps)
-  uint32_t tmem = 0;
-  if (warp >= W_MMA && warp < W_Q) {
-    if (warp == W_MMA) {
-      tmem_alloc(base + C::OFF_MISC, C::COLS);
-      tmem_relinquish();
-    }
-    tc_fence_before();
-    named_bar_sync(BAR_TMEM, (1 + 2 * kSoftWarps) * 32);
-    tc_fence_after();
-    tmem = *tmem_at;
-  }
+  int slots_used = 0;  // of the ring of a copy warp
 
-      // Query rows of a segment -> the B operand of its score MMAs: rows of SW bytes, swizzled,
+  // Query rows of a segment -> the B operand of its score MMAs: rows of SW bytes, swizzled,
       // term j of row r in row j * NQ + r; rows >= G are zero.
       auto stage_q = [&](const Tile& t, int first, int threads) {
         const int par = t.seg & 1;
@@ -618,32 +692,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         fence_proxy_async_smem();
       };
 
-  if (warp == W_K || warp == W_V) {
-    // ------------------------------------------------------------ copy warps
-    const CUtensorMap* map = warp == W_K ? &maps.k : &maps.v;
+  // ---------------------------------------------------------------- copy warps
+  auto copy_tiles = [&] {
+    const bool is_k = warp == W_K || warp == W_K2;
+    const CUtensorMap* map = is_k ? &maps.k : &maps.v;
+    const int ring = is_k ? C::RK : C::RV, slot0 = is_k ? 0 : C::RK;
     const int box = min(a.P, 32);           // rows of a copy
-    const int nbox = kTile / box;
+    const int half = kTile / box / 2;       // boxes of a tile that are this warp's
     const uint32_t box_bytes = box * C::SW * C::CH;
-    const int row = lane * box;             // this lane's box in a tile
+    const int row = (lane + (warp < W_SOFT0 ? 0 : half)) * box;  // this lane's box in a tile
     // the table's entry for this lane's box in a tile; -1: nothing to copy
     auto page_of = [&](const Tile& t) {
-      if (!t.ok || lane >= nbox || row >= t.end - t.pos || t.pos + row + box <= t.lo) return -1;
+      if (!t.ok || lane >= half || row >= t.end - t.pos || t.pos + row + box <= t.lo) return -1;
       return a.table[static_cast<size_t>(t.b) * a.max_pages + ((t.pos + row) >> page_shift)];
     };
     Tile cur = walk.t;
     int page = page_of(cur);
-    for (int i = 0; cur.ok; ++i) {
+    int slot = slot0;
+    uint32_t turn = 1;  // parity of `empty` that lets this turn of the ring begin: none in the first
+    while (cur.ok) {
       next_tile(a, lens, walk);
       const Tile nxt = walk.t;
       const int next_page = page_of(nxt);  // in flight while this tile's copies wait for slots
       const bool there = page >= 0 && page < a.num_pages;
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, there)) * box_bytes;
       const int y = cur.kvh * a.P + ((cur.pos + row) & (a.P - 1));
-      const int e0 = warp == W_K ? C::seq_k(i) : C::seq_v(i, nxt.ok);
 #pragma unroll
       for (int p = 0; p < C::NB; ++p) {
-        const int slot = (e0 + p) % C::RING, use = (e0 + p) / C::RING;
-        if (use > 0) mbar_wait(empty + 8 * slot, (use - 1) & 1, failed);
+        if (slots_used >= ring) warp_wait(empty + 8 * slot, turn, failed);
         const uint32_t fb = full + 8 * slot;
         if (lane == 0) mbar_arrive_expect_tx(fb, bytes);
         __syncwarp();
@@ -653,131 +729,158 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             tma_load_3d(base + slot * C::SLOT + ch * C::CHUNK + row * C::SW, map, p * C::DB + ch * (C::SW / C::EB), y,
                         page, fb);
         }
+        ++slots_used;
+        if (++slot == slot0 + ring) {
+          slot = slot0;
+          turn ^= 1;
+        }
       }
       cur = nxt;
       page = next_page;
-      slots_used += 2 * C::NB;
     }
-  } else if (warp == W_MMA) {
-    // ------------------------------------------------------------- MMA warp
-    // In the ring's order, the whole warp in step; one lane issues. The
-    // descriptors of a slot differ from those of slot 0 by its address.
-    const bool issuer = elect_one();
-    const uint64_t k_desc = smem_desc<C::SW>(base, 16);
-    const uint64_t v_desc = smem_desc<C::SW>(base, C::CH > 1 ? C::CHUNK : C::SLOT);
-    const uint64_t q_desc = smem_desc<C::SW>(base + C::OFF_Q, 16);
-    const uint64_t p_desc = smem_desc<128>(base + C::OFF_P, 16);
-    int slot = 0;
-    uint32_t turn = 0;  // parity of the ring's turn
-    auto advance = [&] {
-      if (++slot == C::RING) {
-        slot = 0;
-        turn ^= 1;
-      }
-    };
-    // bit g, of group g: parity of v_clean's phase, of o_free's, and whether O was used
-    uint32_t cleared = 0, o_phase = 0, o_used = 0;
-    auto scores = [&](int i, const Tile& t) {
-      const int g = i & 1;
-      if (i >= 2) mbar_wait(s_free + 8 * g, ((i - 2) >> 1) & 1, failed);
-      if (t.j == 0) mbar_wait(q_ready + 8 * (t.seg & 1), (t.seg >> 1) & 1, failed);
-      const uint64_t qd = q_desc + (t.seg & 1) * (C::Q_STRIDE >> 4);
-      const uint32_t d = tmem + C::NS * g;
-#pragma unroll
-      for (int p = 0; p < C::NB; ++p) {
-        mbar_wait(full + 8 * slot, turn, failed);
-        tc_fence_after();
-        if (issuer) {
-          const uint64_t kd = k_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
-#pragma unroll
-          for (int ch = 0; ch < C::CH; ++ch)
-#pragma unroll
-            for (int kk = 0; kk < C::SW / 32; ++kk)
-              umma<C::KV8>(d, kd + ((ch * C::CHUNK + 32 * kk) >> 4),
-                           qd + (((p * C::CH + ch) * C::NS * C::SW + 32 * kk) >> 4), C::IDESC_QK, (p | ch | kk) != 0);
-          umma_commit(empty + 8 * slot);
-          if (p == C::NB - 1) {
-            umma_commit(s_full + 8 * g);
-            if (t.j + 1 == t.n) umma_commit(q_free + 8 * (t.seg & 1));
+  };
+
+  // A warpgroup takes its registers in one place, all of its warps together.
+  if (!work) {
+    // nothing but the rows of empty sequences, below
+  } else if (warp < W_SOFT0) {
+    regs_dec<kRegsIssue>();
+    if (warp == W_K || warp == W_V) {
+      copy_tiles();
+    } else if (warp == W_QK) {
+      // ------------------------------------------------------------ scores: S^T = K Q^T
+      // The whole warp in step, one lane issues. The descriptors of a slot differ
+      // from those of slot 0 by its address.
+      const bool issuer = elect_one();
+      const uint64_t k_desc = smem_desc<C::SW>(base, 16);
+      const uint64_t q_desc = smem_desc<C::SW>(base + C::OFF_Q, 16);
+      int slot = 0;
+      uint32_t turn = 0;  // parity of the ring's turn
+      for (int i = 0; walk.t.ok; ++i) {
+        const int g = i & 1, par = walk.t.seg & 1;
+        const bool ends = walk.t.j + 1 == walk.t.n;
+        const uint64_t qd = q_desc + par * (C::Q_STRIDE >> 4);
+        const uint32_t d = tmem + C::NS * g;
+        // the first slot, the S buffer, the segment's query rows: a lane each
+        uint32_t bar = full + 8 * slot, want = turn;
+        if (lane == 1) bar = s_free + 8 * g, want = ((i >> 1) - 1) & 1;
+        if (lane == 2) bar = q_ready + 8 * par, want = (walk.t.seg >> 1) & 1;
+        wait_lanes(bar, want, lane == 0 || (lane == 1 && i >= 2) || (lane == 2 && walk.t.j == 0), failed);
+  #pragma unroll
+        for (int p = 0; p < C::NB; ++p) {
+          if (p > 0) warp_wait(full + 8 * slot, turn, failed);
+          tc_fence_after();
+          if (issuer) {
+            const uint64_t kd = k_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
+  #pragma unroll
+            for (int ch = 0; ch < C::CH; ++ch)
+  #pragma unroll
+              for (int kk = 0; kk < C::SW / 32; ++kk)
+                umma<C::KV8>(d, kd + ((ch * C::CHUNK + 32 * kk) >> 4),
+                             qd + (((p * C::CH + ch) * C::NS * C::SW + 32 * kk) >> 4), C::IDESC_QK, (p | ch | kk) != 0);
+            umma_commit(empty + 8 * slot);
+            if (p == C::NB - 1) {
+              umma_commit(s_full + 8 * g);
+              if (ends) umma_commit(q_free + 8 * par);
+            }
+          }
+          if (++slot == C::RK) {
+            slot = 0;
+            turn ^= 1;
           }
         }
-        advance();
+        next_tile(a, lens, walk);
       }
-    };
-    auto values = [&](int i, const Tile& t) {
-      const int g = i & 1;
-      mbar_wait(p_ready + 8 * g, (i >> 1) & 1, failed);
-      if (t.j < 2) {  // the group's first tile of the segment takes O, once the segment before has left it
-        if ((o_used >> g) & 1) {
-          mbar_wait(o_free + 8 * g, (o_phase >> g) & 1, failed);
-          o_phase ^= 1u << g;
+      // every MMA issued has completed before the tensor memory is released
+      if (issuer) umma_commit(mma_done);
+      bool dfail = false;
+      warp_wait(mma_done, 0, dfail);
+    } else if (warp == W_PV) {
+      // ------------------------------------------------------------ values: O^T += V^T P^T
+      const bool issuer = elect_one();
+      const uint64_t v_desc = smem_desc<C::SW>(base, C::CH > 1 ? C::CHUNK : C::SLOT);
+      const uint64_t p_desc = smem_desc<128>(base + C::OFF_P, 16);
+      int slot = C::RK;
+      uint32_t turn = 0;
+      // bit g, of group g: parity of v_clean's phase, of o_free's, and whether O was used
+      uint32_t cleared = 0, o_phase = 0, o_used = 0;
+      for (int i = 0; walk.t.ok; ++i) {
+        const int g = i & 1;
+        const bool takes = walk.t.j < 2;  // the group's first tile of the segment takes O
+        // the first slot, the weights, and that the group's segment before has left O: a lane each
+        uint32_t bar = full + 8 * slot, want = turn;
+        if (lane == 1) bar = p_ready + 8 * g, want = (i >> 1) & 1;
+        if (lane == 2) bar = o_free + 8 * g, want = (o_phase >> g) & 1;
+        const bool wait_o = takes && ((o_used >> g) & 1);
+        wait_lanes(bar, want, lane < 2 || (lane == 2 && wait_o), failed);
+        if (wait_o) o_phase ^= 1u << g;
+        if (takes) o_used |= 1u << g;
+        // read by every lane before one of them issues what lets the group write the next
+        const bool clear = __any_sync(0xffffffffu, edge[g] != 0);
+        const uint64_t pd = p_desc + g * (C::P_BYTES >> 4);
+        const int nk = (min(kTile, walk.t.end - walk.t.pos) + C::KSTEP - 1) / C::KSTEP;
+        const uint32_t keep = takes ? 0u : 1u;
+  #pragma unroll
+        for (int p = 0; p < C::NB; ++p) {
+          if (p > 0) warp_wait(full + 8 * slot, turn, failed);
+          if (clear) {  // the group clears rows of the slot first
+            if (issuer) mbar_arrive(v_here + 8 * (g * C::NB + p));
+            warp_wait(v_clean + 8 * (g * C::NB + p), (cleared >> g) & 1, failed);
+          }
+          tc_fence_after();
+          if (issuer) {
+            const uint32_t d = tmem + C::O_COL + C::NP * (g * C::NB + p);
+            const uint64_t vd = v_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
+  #pragma unroll
+            for (int kk = 0; kk < kTile / C::KSTEP; ++kk)
+              if (kk < nk)
+                umma<C::KV8>(d, vd + ((kk * C::KSTEP * C::SW) >> 4),
+                             pd + ((kk * 32 / 128 * (C::NP * 128) + kk * 32 % 128) >> 4), C::IDESC_PV, kk > 0 ? 1u : keep);
+            umma_commit(empty + 8 * slot);
+            if (p == C::NB - 1) umma_commit(pv_done + 8 * g);
+          }
+          if (++slot == C::RING) {
+            slot = C::RK;
+            turn ^= 1;
+          }
         }
-        o_used |= 1u << g;
+        if (clear) cleared ^= 1u << g;
+        next_tile(a, lens, walk);
       }
-      const bool clear = edge[g] != 0;
-      const uint64_t pd = p_desc + g * (C::P_BYTES >> 4);
-      const int nk = (min(kTile, t.end - t.pos) + C::KSTEP - 1) / C::KSTEP;
-      const uint32_t keep = t.j > 1 ? 1u : 0u;
-#pragma unroll
-      for (int p = 0; p < C::NB; ++p) {
-        mbar_wait(full + 8 * slot, turn, failed);
-        if (clear) {  // the group clears rows of the slot first
-          if (issuer) mbar_arrive(v_here + 8 * (g * C::NB + p));
-          mbar_wait(v_clean + 8 * (g * C::NB + p), (cleared >> g) & 1, failed);
-        }
-        tc_fence_after();
-        if (issuer) {
-          const uint32_t d = tmem + C::O_COL + C::NP * (g * C::NB + p);
-          const uint64_t vd = v_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
-#pragma unroll
-          for (int kk = 0; kk < kTile / C::KSTEP; ++kk)
-            if (kk < nk)
-              umma<C::KV8>(d, vd + ((kk * C::KSTEP * C::SW) >> 4),
-                           pd + ((kk * 32 / 128 * (C::NP * 128) + kk * 32 % 128) >> 4), C::IDESC_PV, kk > 0 ? 1u : keep);
-          umma_commit(empty + 8 * slot);
-          if (p == C::NB - 1) umma_commit(pv_done + 8 * g);
-        }
-        advance();
-      }
-      if (clear) cleared ^= 1u << g;
-    };
-    Tile cur = walk.t;
-    scores(0, cur);
-    for (int i = 0; cur.ok; ++i) {
-      next_tile(a, lens, walk);
-      const Tile nxt = walk.t;
-      if (nxt.ok) scores(i + 1, nxt);
-      values(i, cur);
-      cur = nxt;
+      if (issuer) umma_commit(mma_done + 8);
+      bool dfail = false;
+      warp_wait(mma_done + 8, 0, dfail);
     }
-    // every MMA issued has completed before the tensor memory is released
-    if (issuer) umma_commit(mma_done);
-    bool dfail = false;
-    mbar_wait(mma_done, 0, dfail);
-  } else if (warp == W_Q) {
-    // ------------------------------------------------ query rows, from the second segment on
-    for (;;) {
-      walk.t.j = walk.t.n;  // on to the next segment
-      next_tile(a, lens, walk);
-      if (!walk.t.ok) break;
-      const int seg = walk.t.seg;
-      if (seg >= 2) mbar_wait(q_free + 8 * (seg & 1), ((seg - 2) >> 1) & 1, failed);
-      stage_q(walk.t, lane, 32);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready + 8 * (seg & 1));
-    }
-    // the unit that the share's end cuts, if it does: for the merge
-    if (lane == 0) {
-      Cut cut{walk.t.b, walk.t.kvh, -1, -1};
-      if (!walk.t.ends) {
-        const long long u0 = per * (c + 1) - walk.g0;  // a share that ends inside a band is a full one
-        cut.c0 = static_cast<int>(u0 / per);
-        cut.c1 = static_cast<int>((u0 + walk.d.granules - 1) / per);
+  } else if (warp >= W_Q) {
+    regs_dec<kRegsHelp>();
+    if (warp == W_K2 || warp == W_V2) {
+      copy_tiles();
+    } else if (warp == W_Q) {
+      // ------------------------------------------------ query rows, from the second segment on
+      for (;;) {
+        walk.t.j = walk.t.n;  // on to the next segment
+        next_tile(a, lens, walk);
+        if (!walk.t.ok) break;
+        const int seg = walk.t.seg;
+        if (seg >= 2) warp_wait(q_free + 8 * (seg & 1), ((seg - 2) >> 1) & 1, failed);
+        stage_q(walk.t, lane, 32);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready + 8 * (seg & 1));
       }
-      cuts[c] = cut;
+      // the unit that the share's end cuts, if it does: for the merge
+      if (lane == 0) {
+        Cut cut{walk.t.b, walk.t.kvh, -1, -1};
+        if (!walk.t.ends) {
+          const long long u0 = per * (c + 1) - walk.g0;  // a share that ends inside a band is a full one
+          cut.c0 = static_cast<int>(u0 / per);
+          cut.c1 = static_cast<int>((u0 + walk.d.granules - 1) / per);
+        }
+        cuts[c] = cut;
+      }
     }
   } else {
     // ---------------------------------------------- softmax / epilogue warps
+    regs_inc<kRegsSoft>();
     constexpr float kLazy = C::KV8 ? kLazy8 : kLazy16, kBias = C::KV8 ? kBias8 : kBias16;
     const int grp = (warp - W_SOFT0) / kSoftWarps;  // takes the tiles i with i % 2 == grp
     const int sw = (warp - W_SOFT0) % kSoftWarps;
@@ -812,12 +915,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     named_bar_sync(BAR_BOTH, 2 * kSoft);
     if (grp == 0 && tq == 0) mbar_arrive(q_ready);
 
-    // This group's tiles: the current one and the next. `more`: some tile follows the current one.
+    // This group's tiles: the current one and the next.
     if (grp == 1) next_tile(a, lens, walk);
     Tile cur = walk.t;
     int page = entry(cur);
     next_tile(a, lens, walk);
-    bool more = walk.t.ok;
     next_tile(a, lens, walk);
     Tile nxt = walk.t;
     int next_page = entry(nxt);
@@ -831,7 +933,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     int i = grp, seg_seen = -1, cleared = 0;
     while (cur.ok) {
       next_tile(a, lens, walk);
-      const bool next_more = walk.t.ok;
       next_tile(a, lens, walk);
       const Tile after = walk.t;
       const int after_page = entry(after);
@@ -850,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       const int rows = (min(kTile, cur.end - cur.pos) + C::KSTEP - 1) / C::KSTEP * C::KSTEP;  // that P.V reads
       const bool dead_row = !live && pl < rows;
 
-      mbar_wait(s_full + 8 * grp, u & 1, failed);
+      warp_wait(s_full + 8 * grp, u & 1, failed);
       tc_fence_after();
       float s[C::NS];
       tmem_load<C::NS>(tmem + tlane + C::NS * grp, s);
@@ -906,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           resc |= need;
         }
         if (resc && cur.j > 1) {  // O holds the group's earlier tiles of the segment: rescale it once they are done
-          mbar_wait(pv_done + 8 * grp, (u - 1) & 1, failed);
+          warp_wait(pv_done + 8 * grp, (u - 1) & 1, failed);
           tc_fence_after();
 #pragma unroll 1
           for (int x = 0; x < C::NB * C::NP; x += 16) {
@@ -928,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       }
 
       // P(i) -> the group's buffer; its last reader, P.V(i - 2), must be done
-      if (u >= 1) mbar_wait(pv_done + 8 * grp, (u - 1) & 1, failed);
+      if (u >= 1) warp_wait(pv_done + 8 * grp, (u - 1) & 1, failed);
       if (tq == 0) edge[grp] = clear;
       unsigned char* pbuf = smem + C::OFF_P + grp * C::P_BYTES;
       if constexpr (C::KV8) {
@@ -965,8 +1066,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       if (clear) {
 #pragma unroll 1
         for (int p = 0; p < C::NB; ++p) {
-          const int slot = (C::seq_v(i, more) + p) % C::RING;
-          mbar_wait(v_here + 8 * (grp * C::NB + p), cleared & 1, failed);
+          const int slot = C::RK + (i * C::NB + p) % C::RV;
+          warp_wait(v_here + 8 * (grp * C::NB + p), cleared & 1, failed);
           if (dead_row) {
 #pragma unroll 1
             for (int x = 0; x < C::SW * C::CH; x += 16)
@@ -993,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           if (sw == 0) refs[lane / kPer] = ref_lane;
         }
         named_bar_sync(BAR_GROUP + grp, kSoft);
-        mbar_wait(pv_done + 8 * grp, u & 1, failed);
+        warp_wait(pv_done + 8 * grp, u & 1, failed);
         if (tq < C::NQ) {
           const float4 t4 = *reinterpret_cast<const float4*>(sums + tq * kSoftWarps);
           stat[grp * C::NQ + tq] = make_float2(refs[tq], (t4.x + t4.y) + (t4.z + t4.w));  // fixed order
@@ -1060,7 +1161,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         mbar_arrive(o_free + 8 * grp);
         mbar_arrive(o_free + 8 * (both ? 1 - grp : grp));
       }
-      more = next_more;
       cur = nxt;
       page = next_page;
       ksvs = next_ksvs;
@@ -1070,19 +1170,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     }
   }
 
+  // Rows of empty sequences are zero.
+  for (int b = c; b < a.B; b += gridDim.x) {
+    if ((a.B <= kLenCache ? lens[b] : clamp_len(a, a.lens[b])) > 0) continue;
+    for (int i = tid; i < a.NH * C::HS; i += kThreads) {
+      const size_t o = static_cast<size_t>(b) * a.NH * C::HS + i;
+      a.out[o] = 0;
+      if (a.out_f32) a.out_f32[o] = 0.f;
+    }
+  }
+
   // release the tensor memory once every warp is done with it
   tc_fence_before();
   __syncthreads();
-  if (warp == W_MMA) {
+  if (warp == W_QK) {
     tc_fence_after();
     tmem_dealloc(tmem, C::COLS);
   }
   // No copy may be in flight when the block leaves, also where a wait gave up:
   // the last phase of each slot (bounded, own flag).
-  if (warp == W_V) {
+  if (work && (warp == W_K || warp == W_V)) {
+    const int ring = warp == W_K ? C::RK : C::RV, slot0 = warp == W_K ? 0 : C::RK;
     bool dfail = false;
-    for (int k = 0; k < C::RING && k < slots_used; ++k)
-      mbar_wait(full + 8 * k, ((slots_used - 1 - k) / C::RING) & 1, dfail);
+    for (int k = 0; k < ring && k < slots_used; ++k)
+      warp_wait(full + 8 * (slot0 + k), ((slots_used - 1 - k) / ring) & 1, dfail);
   }
 }
 
@@ -1101,9 +1212,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   grid_dependency_wait();
   grid_launch_dependents();
   const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.NH / a.NKV;
   const Cut cut = reinterpret_cast<const Cut*>(a.cuts)[c];
   if (cut.c0 < 0) return;
-  const int G = a.NH / a.NKV, row_items = a.HS / 4, items = G * row_items;
+  const int row_items = a.HS / 4, items = G * row_items;
   const int helpers = cut.c1 - cut.c0, parts = helpers + 1;
   const int each = (items + helpers - 1) / helpers;
   const int i0 = (c - cut.c0) * each, i1 = min(items, i0 + each);
@@ -1112,51 +1224,60 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   // the share c0 holds the unit's beginning, the others continue it
   auto slot_of = [&](int part) { return 2 * (cut.c0 + part) + (part == 0 ? 1 : 0); };
   const float2* ml = reinterpret_cast<const float2*>(a.ws_ml);
-  for (int r = r0 + warp; r <= r1; r += kMergeThreads / 32) {
-    float m = kNegInf;  // every part has a finite reference
-    for (int p = lane; p < parts; p += 32) m = fmaxf(m, ml[static_cast<size_t>(slot_of(p)) * G + r].x);
-    for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    float l = 0.f;
-    for (int p = lane; p < parts; p += 32) {
-      const float2 x = ml[static_cast<size_t>(slot_of(p)) * G + r];
-      const float f = exp2f(x.x - m);
-      factor[(r - r0) * parts + p] = f;
-      l += f * x.y;
-    }
-    for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
-    if (lane == 0) inv[r] = l;
-  }
-  __syncthreads();
+  const float4* parts_o = reinterpret_cast<const float4*>(a.ws_o);
   for (int base = i0; base < i1; base += kMergeThreads) {
     const int n = min(kMergeThreads, i1 - base);  // items of this turn
     const int groups = kMergeThreads / n;         // threads of an item
     const int item = base + tid % n, g = tid / n;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     const int r = item / row_items, d = item % row_items;
-    if (g < groups) {
-      const float* f = factor + (r - r0) * parts;
-#pragma unroll 8
-      for (int p = g; p < parts; p += groups) {
-        const float4 x = reinterpret_cast<const float4*>(a.ws_o)[(static_cast<size_t>(slot_of(p)) * G + r) * row_items + d];
-        const float w = f[p];
-        s.x += w * x.x;
-        s.y += w * x.y;
-        s.z += w * x.z;
-        s.w += w * x.w;
+    // the first partials are on their way while the factors are made
+    constexpr int kAhead = 8;
+    float4 x[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int p = g + j * groups;
+      x[j] = g < groups && p < parts ? parts_o[(static_cast<size_t>(slot_of(p)) * G + r) * row_items + d]
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (base == i0) {
+      for (int q = r0 + warp; q <= r1; q += kMergeThreads / 32) {
+        float m = kNegInf;  // every part has a finite reference
+        for (int p = lane; p < parts; p += 32) m = fmaxf(m, ml[static_cast<size_t>(slot_of(p)) * G + q].x);
+        for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+        float l = 0.f;
+        for (int p = lane; p < parts; p += 32) {
+          const float2 y = ml[static_cast<size_t>(slot_of(p)) * G + q];
+          const float f = exp2f(y.x - m);
+          factor[(q - r0) * parts + p] = f;
+          l += f * y.y;
+        }
+        for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+        if (lane == 0) inv[q] = l == 0.f ? 0.f : 1.f / l;
       }
+      __syncthreads();
+    }
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* f = factor + (r - r0) * parts;
+    auto add = [&](const float4& y, float w) {
+      s.x += w * y.x;
+      s.y += w * y.y;
+      s.z += w * y.z;
+      s.w += w * y.w;
+    };
+    if (g < groups) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (g + j * groups < parts) add(x[j], f[g + j * groups]);
+#pragma unroll 4
+      for (int p = g + kAhead * groups; p < parts; p += groups)
+        add(parts_o[(static_cast<size_t>(slot_of(p)) * G + r) * row_items + d], f[p]);
       acc[tid] = s;
     }
     __syncthreads();
     if (g == 0) {
-      for (int j = 1; j < groups; ++j) {
-        const float4 x = acc[j * n + tid];
-        s.x += x.x;
-        s.y += x.y;
-        s.z += x.z;
-        s.w += x.w;
-      }
-      const float l = inv[r];
-      const float4 y = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(s.x / l, s.y / l, s.z / l, s.w / l);
+      for (int j = 1; j < groups && j < parts; ++j) add(acc[j * n + tid], 1.f);
+      const float by = inv[r];
+      const float4 y = make_float4(s.x * by, s.y * by, s.z * by, s.w * by);
       const size_t at = (static_cast<size_t>(cut.b) * a.NH + static_cast<size_t>(cut.kvh) * G + r) * a.HS + 4 * d;
       const uint32_t lo = f32_to_bf16_bits(y.x) | (static_cast<uint32_t>(f32_to_bf16_bits(y.y)) << 16);
       const uint32_t hi = f32_to_bf16_bits(y.z) | (static_cast<uint32_t>(f32_to_bf16_bits(y.w)) << 16);
