@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       const bool there = page >= 0 && page < a.num_pages;
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, there)) * box_bytes;
       const int y = cur.kvh * a.P + ((cur.pos + row) & (a.P - 1));
-#pragma unroll
+#pragma unroll 1
       for (int p = 0; p < C::NB; ++p) {
         if (slots_used >= ring) warp_wait(empty + 8 * slot, turn, failed);
         const uint32_t fb = full + 8 * slot;
@@ -766,18 +766,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         if (lane == 1) bar = s_free + 8 * g, want = ((i >> 1) - 1) & 1;
         if (lane == 2) bar = q_ready + 8 * par, want = (walk.t.seg >> 1) & 1;
         wait_lanes(bar, want, lane == 0 || (lane == 1 && i >= 2) || (lane == 2 && walk.t.j == 0), failed);
-  #pragma unroll
+  #pragma unroll 1
         for (int p = 0; p < C::NB; ++p) {
           if (p > 0) warp_wait(full + 8 * slot, turn, failed);
           tc_fence_after();
           if (issuer) {
+            const uint64_t qp = qd + p * ((C::CH * C::NS * C::SW) >> 4);
             const uint64_t kd = k_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
   #pragma unroll
             for (int ch = 0; ch < C::CH; ++ch)
   #pragma unroll
               for (int kk = 0; kk < C::SW / 32; ++kk)
                 umma<C::KV8>(d, kd + ((ch * C::CHUNK + 32 * kk) >> 4),
-                             qd + (((p * C::CH + ch) * C::NS * C::SW + 32 * kk) >> 4), C::IDESC_QK, (p | ch | kk) != 0);
+                             qp + ((ch * C::NS * C::SW + 32 * kk) >> 4), C::IDESC_QK, (p | ch | kk) != 0);
             umma_commit(empty + 8 * slot);
             if (p == C::NB - 1) {
               umma_commit(s_full + 8 * g);
@@ -820,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const uint64_t pd = p_desc + g * (C::P_BYTES >> 4);
         const int nk = (min(kTile, walk.t.end - walk.t.pos) + C::KSTEP - 1) / C::KSTEP;
         const uint32_t keep = takes ? 0u : 1u;
-  #pragma unroll
+  #pragma unroll 1
         for (int p = 0; p < C::NB; ++p) {
           if (p > 0) warp_wait(full + 8 * slot, turn, failed);
           if (clear) {  // the group clears rows of the slot first
@@ -831,11 +832,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           if (issuer) {
             const uint32_t d = tmem + C::O_COL + C::NP * (g * C::NB + p);
             const uint64_t vd = v_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
-  #pragma unroll
-            for (int kk = 0; kk < kTile / C::KSTEP; ++kk)
-              if (kk < nk)
-                umma<C::KV8>(d, vd + ((kk * C::KSTEP * C::SW) >> 4),
-                             pd + ((kk * 32 / 128 * (C::NP * 128) + kk * 32 % 128) >> 4), C::IDESC_PV, kk > 0 ? 1u : keep);
+              auto step = [&](int kk) {
+              umma<C::KV8>(d, vd + ((kk * C::KSTEP * C::SW) >> 4),
+                           pd + ((kk * 32 / 128 * (C::NP * 128) + kk * 32 % 128) >> 4), C::IDESC_PV, kk > 0 ? 1u : keep);
+            };
+            constexpr int kSteps = kTile / C::KSTEP;
+            if (nk == kSteps) {
+#pragma unroll
+              for (int kk = 0; kk < kSteps; ++kk) step(kk);
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < nk; ++kk) step(kk);
+            }
             umma_commit(empty + 8 * slot);
             if (p == C::NB - 1) umma_commit(pv_done + 8 * g);
           }
