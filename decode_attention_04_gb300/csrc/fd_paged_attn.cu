@@ -3,8 +3,11 @@
 // sequence, K and V bf16 or E4M3 with a scale for each page and head.
 //
 // Work. The live bands of all (sequence, KV head) units lie one behind the
-// other in granules of 32 positions; block c of C takes the granules [c, c + 1)
-// * ceil(total / C). So every SM reads the same number of bytes whatever the lengths are,
+// other in granules of 32 positions, each behind a gap of `min_share` granules
+// that stands for what beginning and ending a band costs a block (about as
+// much as copying 64 KB; without it the block that had the eight heads of a
+// short sequence held up a ragged batch by a fifth). Block c of C takes the places [c, c + 1)
+// * ceil(total / C). So every SM has the same work whatever the lengths are,
 // in one wave, and a block leaves at most two partials: of a band that began
 // before its share and of one that goes on behind it. A band inside one share
 // is written to the output directly.
@@ -261,14 +264,19 @@ struct Tile {
 
 // Walks a block's tiles in order.
 struct Walk {
-  long long left;  // granules of the share that are still to come
-  int kvh, g0;     // where the next segment begins: head, granule of the band
+  long long left;  // places of the share that are still to come
+  int kvh, g0;     // where the next segment begins: head, place of the band (gap, then granules)
   Band d;          // of sequence t.b
   Tile t;
 };
 
 __device__ __forceinline__ Band band_of_seq(const PagedArgs& a, const int* cache, int b) {
   return band_from(a, a.B <= kLenCache ? cache[b] : clamp_len(a, a.lens[b]));
+}
+
+// Places of one unit in the stream; none where there is no position.
+__device__ __forceinline__ int places(const PagedArgs& a, const Band& d) {
+  return d.granules > 0 ? d.granules + a.min_share : 0;
 }
 
 __device__ __forceinline__ void next_tile(const PagedArgs& a, const int* cache, Walk& w) {
@@ -283,22 +291,34 @@ __device__ __forceinline__ void next_tile(const PagedArgs& a, const int* cache, 
     t.n = 0;
     return;
   }
-  while (w.g0 >= w.d.granules) {  // the band is done: the next head, or the next sequence that has one
+  int b = t.b;
+  while (w.g0 >= places(a, w.d)) {  // the band is done: the next head, or the next sequence that has one
     w.g0 = 0;
     if (++w.kvh >= a.NKV || w.d.granules == 0) {
       w.kvh = 0;
-      w.d = band_of_seq(a, cache, ++t.b);
+      w.d = band_of_seq(a, cache, ++b);
     }
   }
-  const int take = static_cast<int>(min(static_cast<long long>(w.d.granules - w.g0), w.left));
+  if (w.g0 < a.min_share) {  // the gap
+    const int skip = static_cast<int>(min(static_cast<long long>(a.min_share - w.g0), w.left));
+    w.left -= skip;
+    w.g0 += skip;
+    if (w.left <= 0) {
+      t.ok = false;
+      t.n = 0;
+      return;
+    }
+  }
+  const int take = static_cast<int>(min(static_cast<long long>(places(a, w.d) - w.g0), w.left));
   w.left -= take;
+  t.b = b;
   t.seg += 1;
   t.kvh = w.kvh;
   t.lo = w.d.lo;
-  t.pos = (w.d.lo / kGranule + w.g0) * kGranule;
-  t.begins = w.g0 == 0;
+  t.pos = (w.d.lo / kGranule + w.g0 - a.min_share) * kGranule;
+  t.begins = w.g0 == a.min_share;
   w.g0 += take;
-  t.ends = w.g0 == w.d.granules;
+  t.ends = w.g0 == places(a, w.d);
   t.end = t.ends ? w.d.len : t.pos + take * kGranule;
   t.j = 0;
   t.n = (t.end - t.pos + kTile - 1) / kTile;
@@ -492,20 +512,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // This block's share of the granules, and where it begins.
+  // This block's share of the places, and where it begins.
   long long per, total;
   Walk walk;
   walk.t.ok = false;
   walk.t.seg = -1;
   walk.t.j = walk.t.n = 0;
   walk.t.b = walk.kvh = walk.g0 = 0;
-  auto shares = [&](long long heads_granules) {  // granules of one head of every sequence
-    total = heads_granules * a.NKV;
+  auto shares = [&](long long of_a_head) {  // places of one head of every sequence
+    total = of_a_head * a.NKV;
     per = total <= 0x7fff0000ll ? static_cast<int>(total + a.blocks - 1) / a.blocks : (total + a.blocks - 1) / a.blocks;
     per = max(per, static_cast<long long>(a.min_share));
     walk.left = min(per, total - per * c);
   };
-  // sequence b, whose bands have x granules each and begin at granule off of the stream, holds the share's first
+  // sequence b, whose units have x places each and begin at place off of the stream, holds the share's first
   auto begin_at = [&](int b, long long off, int x) {
     const long long in = per * c - off;
     walk.t.b = b;
@@ -529,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       if (raw_len < 0) flags |= FD_DEVERR_LEN_NEGATIVE;
       if (raw_len > len) flags |= FD_DEVERR_LEN_CLAMPED;
       if (b < a.B) lens[b] = len;  // each warp writes the same, and reads its own
-      x[k] = band_from(a, len).granules;
+      x[k] = places(a, band_from(a, len));
       before[k] = static_cast<int>(mine);
       mine += x[k];
     }
@@ -571,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       if (raw_len < 0) flags |= FD_DEVERR_LEN_NEGATIVE;
       if (raw_len > len) flags |= FD_DEVERR_LEN_CLAMPED;
       if (a.B <= kLenCache) lens[b] = len;
-      mine += band_from(a, len).granules;
+      mine += places(a, band_from(a, len));
     }
     if (c == 0 && flags) atomicOr(&g_device_error, flags);
     for (int i = 16; i; i >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, i);
@@ -581,10 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     for (int i = 0; i < kThreads / 32; ++i) all += sums[i];
     shares(all);
     const long long start = per * c;
-    long long before = 0;  // granules (of one head) of the sequences before this chunk
+    long long before = 0;  // places (of one head) of the sequences before this chunk
     for (int b0 = 0; b0 < a.B && start < total; b0 += kThreads) {
       const int b = b0 + tid;
-      const int x = b < a.B ? band_of_seq(a, lens, b).granules : 0;
+      const int x = b < a.B ? places(a, band_of_seq(a, lens, b)) : 0;
       long long inc = x;
       for (int i = 1; i < 32; i <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, inc, i);
@@ -615,11 +635,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       walk.g0 = share_at[2];
     }
   }
-  const bool work = walk.left > 0;
-  if (work) {
+  if (walk.left > 0) {
     walk.d = band_of_seq(a, lens, walk.t.b);
     next_tile(a, lens, walk);
   }
+  const bool work = walk.t.ok;
 
   Cut* cuts = reinterpret_cast<Cut*>(a.cuts);
   if (!work && tid == 0) cuts[c].c0 = -1;
@@ -879,7 +899,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       if (lane == 0) {
         Cut cut{walk.t.b, walk.t.kvh, -1, -1};
         if (!walk.t.ends) {
-          const long long u0 = per * (c + 1) - walk.g0;  // a share that ends inside a band is a full one
+          // of the band's first granule; a share that ends inside a band is a full one
+          const long long u0 = per * (c + 1) - walk.g0 + a.min_share;
           cut.c0 = static_cast<int>(u0 / per);
           cut.c1 = static_cast<int>((u0 + walk.d.granules - 1) / per);
         }

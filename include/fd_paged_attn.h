@@ -54,7 +54,8 @@ enum {
 
 /*
  * Plan of fd_paged_attn_ex. The work is the stream of every (sequence, KV
- * head)'s live band, cut into pieces of `granule` positions and dealt to
+ * head)'s live band in pieces of `granule` positions, each band counted as
+ * `min_share` pieces more than it has, and dealt to
  * `blocks` thread blocks in equal consecutive shares on the device (the
  * lengths are read there): a block may end one band and begin the next. A band
  * that lies in several shares leaves one (O, m, l) partial in each, which a
@@ -63,7 +64,7 @@ enum {
 typedef struct {
   int blocks;             /* thread blocks of the attention kernel (persistent) */
   int granule;            /* positions: shares begin at multiples of it in a band */
-  int min_share;          /* a block's share is at least this many granules */
+  int min_share;          /* a block's share is at least this many granules, and a band counts as that many more */
   int num_sms;            /* SM count the plan assumed */
   int kv_dtype;           /* FD_KV_BF16 or FD_KV_E4M3 */
   size_t workspace_bytes; /* bytes of workspace fd_paged_attn_ex needs; no byte of it needs a value */

@@ -773,3 +773,43 @@ def test_decode_step_in_a_graph():
                               dev.book.lens, 0, HS ** -0.5, N)
     assert (np.abs(out.double().cpu().numpy() - want) <= np.abs(want) * 2.0 ** -8 + 2.0 ** -10 * big[..., None]).all()
     assert fd.fd_get_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("HS,NKV,G,P,lens", [
+    (64, 8, 4, 16, [131000, 70001, 63, 59000]), (128, 8, 4, 16, [120000, 1, 90007]), (512, 1, 16, 128, [262144, 200001]),
+    (256, 4, 9, 32, [100000, 64, 101, 99999])])
+def test_attn_long_shares(kv, HS, NKV, G, P, lens):
+    """Shares of many tiles, run several times without a pause: against 64-bit attention of some heads, made on the GPU, and
+    bit for bit the same every time."""
+    wide = -(-max(lens) // P)
+    N = sum(-(-n // P) for n in lens)
+    table = make_table(lens, P, wide, N, 5)
+    gen = torch.Generator(device=DEV).manual_seed(HS)
+    shape = (N, NKV, P, HS)
+    k, v = (torch.randn(shape, generator=gen, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    ks = vs = None
+    if kv == E4M3:
+        ks, vs = (torch.exp2(torch.randint(-8, -5, (N, NKV), generator=gen, device=DEV).float()) for _ in range(2))
+        k, v = ((x * 64).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) for x in (k, v))
+    B, NH = len(lens), NKV * G
+    q = torch.randn(B, NH, HS, generator=gen, device=DEV).bfloat16()
+    td, ld = d(table), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    fd.fd_get_device_error()
+    outs = [fd.paged_attention(q, k, v, td, ld, k_scale=ks, v_scale=vs) for _ in range(6)]
+    assert fd.fd_get_device_error() == 0
+    assert all(torch.equal(outs[0].view(torch.int16), x.view(torch.int16)) for x in outs[1:])
+    val = torch.from_numpy(ref.TABLE).to(DEV)
+    for b, n in enumerate(lens):
+        pos = torch.arange(n, device=DEV)
+        page, slot = td[b].long()[pos // P], pos % P
+        for h in (0, NKV - 1):
+            kk, vv = k[page, h, slot], v[page, h, slot]
+            if kv == E4M3:
+                kk, vv = val[kk.long()] * ks[page, h].double()[:, None], val[vv.long()] * vs[page, h].double()[:, None]
+            kk, vv, qq = kk.double(), vv.double(), q[b, h * G:(h + 1) * G].double()
+            want = torch.softmax(qq @ kk.T * HS ** -0.5, 1) @ vv
+            mass = (qq.abs() @ kk.abs().T).amax(1, keepdim=True) * HS ** -0.5
+            lim = (4 * HS * 2.0 ** -23 * mass + (2.0 ** -11 if kv == E4M3 else 2.0 ** -16) + 2.0 ** -20) * vv.abs().max()
+            got = outs[0][b, h * G:(h + 1) * G].double()
+            assert ((got - want).abs() <= lim + want.abs() * 2.0 ** -8).all()
