@@ -286,6 +286,8 @@ def _fast():
     libfd.so) when they were built and that library is the one loaded; else
     None, and calls go through ctypes."""
     global _fast_mod, _fast_for
+    if _fast_for is not None and _fast_for is _lib:
+        return _fast_mod
     lib = load_library()
     if _fast_for is not lib:
         _fast_for, _fast_mod = lib, None
@@ -392,13 +394,20 @@ def decode_attention(q, k_cache, v_cache, lens, window=0, scale=0.0, out=None, s
 # ------------------------------------------------------- the cache in pages
 
 
+_current_raw = None
+
+
 def _raw_stream(stream) -> int:
     """As _stream; the current stream without an object made for it, where torch offers that."""
+    global _current_raw
     if stream is not None:
         return _stream(stream) or 0
-    import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(torch.cuda.current_device()) if get else _stream(None) or 0
+    if _current_raw is None:
+        import torch
+        torch.cuda.current_device()  # initialises CUDA
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        _current_raw = (lambda: raw(device())) if raw and device else (lambda: _stream(None) or 0)
+    return _current_raw()
 
 
 

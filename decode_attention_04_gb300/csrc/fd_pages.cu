@@ -17,6 +17,14 @@ namespace {
 
 #include "fd_device.cuh"
 
+// Every kernel here is launched before the one ahead of it on the stream has
+// ended (programmatic dependent launch), and waits for that before it touches
+// memory: its launch is out of the way by then.
+__device__ __forceinline__ void begin_kernel() {
+  grid_dependency_wait();
+  grid_launch_dependents();
+}
+
 // ================================================================== appending
 
 // Tokens of one sequence that fall into one page.
@@ -106,33 +114,41 @@ __device__ __forceinline__ float block_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
 }
 
-// Codes of x / s. A power of two (every scale that this writer makes) divides
-// exactly by a product with its reciprocal.
-struct Divisor {
-  float s, inv;
-  bool pow2;
-  __device__ explicit Divisor(float scale) : s(scale) {
-    const uint32_t u = __float_as_uint(scale);
-    pow2 = (u & 0x7fffffu) == 0 && u >= 0x00800000u && u < 0x7e800000u;  // 2^-126 .. 2^125
-    inv = pow2 ? __uint_as_float(0x7f000000u - u) : 0.f;
-  }
-  __device__ float operator()(float x) const { return pow2 ? x * inv : (s > 0.f ? x / s : 0.f); }
-};
-
 __device__ __forceinline__ uint16_t quantise2(float x, float y) {
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
 
-__device__ __forceinline__ float finite_or_nan(float x) { return isfinite(x) ? x : __int_as_float(0x7fffffff); }
-
-// 8 bf16 values -> 8 codes.
-__device__ __forceinline__ uint2 quantise8(const uint4& v, const Divisor& by) {
+// Codes of 8 values over a power of two (every scale that this writer makes),
+// which divides exactly by a product with its reciprocal. All values finite.
+__device__ __forceinline__ uint2 quantise8(const uint4& v, float inv) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    c[i] = quantise2(by(finite_or_nan(__uint_as_float(u[i] << 16))), by(finite_or_nan(__uint_as_float(u[i] & 0xffff0000u))));
+    c[i] = quantise2(__uint_as_float(u[i] << 16) * inv, __uint_as_float(u[i] & 0xffff0000u) * inv);
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// The same for any scale and any values: NaN where x is not finite, 0 where
+// s is 0. Out of line: the divisions' code would crowd the rest out of the
+// instruction cache.
+__device__ __noinline__ uint2 quantise8_any(uint4 v, float s) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    float x[2] = {__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u)};
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) x[k] = isfinite(x[k]) ? (s > 0.f ? x[k] / s : 0.f) : __int_as_float(0x7fffffff);
+    c[i] = quantise2(x[0], x[1]);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// The reciprocal of a power of two in [2^-126, 2^125], else 0.
+__device__ __forceinline__ float pow2_reciprocal(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x7fffffu) == 0 && u >= 0x00800000u && u < 0x7e800000u ? __uint_as_float(0x7f000000u - u) : 0.f;
 }
 
 // The codes of four values, multiplied.
@@ -140,6 +156,21 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
   const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(c & 0xffff), __NV_E4M3)));
   const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(c >> 16), __NV_E4M3)));
   return quantise2(a.x * ratio, a.y * ratio) | (static_cast<uint32_t>(quantise2(b.x * ratio, b.y * ratio)) << 16);
+}
+
+// The largest of an item's values (WPI warps; all warps of the block call it).
+template <int WPI>
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
+  m = __reduce_max_sync(0xffffffffu, m);
+  if constexpr (WPI > 1) {
+    const int warp = threadIdx.x >> 5;
+    __syncthreads();  // red may still be read from a call before
+    if ((threadIdx.x & 31) == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WPI; ++i) m = max(m, red[warp / WPI * WPI + i]);
+  }
+  return m;
 }
 
 // An item - one head's K or V of a unit - belongs to WPI warps, each thread of
@@ -153,6 +184,7 @@ __global__ void __launch_bounds__(WPI > 8 ? WPI * 32 : 256) append_kernel(const 
   constexpr int kItems = kBlock / 32 / WPI;
   __shared__ uint32_t red[kBlock / 32];
   const int tid = threadIdx.x, lane = tid & 31;
+  begin_kernel();
   const Segment g = find_segment(a, blockIdx.x, lane, blockIdx.y == 0 && tid == 0);
   if (g.n <= 0) return;
   const int item = blockIdx.y * kItems + tid / (32 * WPI);
@@ -179,25 +211,29 @@ __global__ void __launch_bounds__(WPI > 8 ? WPI * 32 : 256) append_kernel(const 
   } else {
     float* scale = (w ? a.scale[1] : a.scale[0]) + block;
     const float old = there && g.slot > 0 ? *scale : 0.f;
-    // the largest |x| by its bits, two at a time; not finite ones only count as 0
+    // the largest |x| by its bits, two at a time
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    for (int i = 0; i < VPT; ++i)
+      m = __vmaxu2(__vmaxu2(__vmaxu2(m, v[i].x & 0x7fff7fffu), __vmaxu2(v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu)),
+                   v[i].w & 0x7fff7fffu);
+    m = block_max<WPI>(max(m & 0xffffu, m >> 16), red);
+    const bool finite = m < 0x7f80u;
+    if (!finite) {  // once more, without the values that are not
+      m = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t abs2 = u[k] & 0x7fff7fffu;
-        m = __vmaxu2(m, abs2 & ~__vcmpgeu2(abs2, 0x7f807f80u));
+      for (int i = 0; i < VPT; ++i) {
+        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t abs2 = u[k] & 0x7fff7fffu;
+          m = __vmaxu2(m, abs2 & ~__vcmpgeu2(abs2, 0x7f807f80u));
+        }
       }
+      m = max(m & 0xffffu, m >> 16);
     }
-    m = max(m & 0xffffu, m >> 16);
-    m = __reduce_max_sync(0xffffffffu, m);
-    if constexpr (WPI > 1) {
-      if (lane == 0) red[tid >> 5] = m;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < WPI; ++i) m = max(m, red[tid / (32 * WPI) * WPI + i]);
-    }
+    // every warp of a block that has several items comes here if one does
+    if (WPI == 1 ? !finite : __syncthreads_or(!finite)) m = block_max<WPI>(m, red);
     if (!there) return;
     const float s = fmaxf(block_scale(__uint_as_float(m << 16)), old);
     uint8_t* pages = static_cast<uint8_t*>(w ? a.pages[1] : a.pages[0]);
@@ -209,11 +245,17 @@ __global__ void __launch_bounds__(WPI > 8 ? WPI * 32 : 256) append_kernel(const 
         held[i] = make_uint4(rescale4(c.x, ratio), rescale4(c.y, ratio), rescale4(c.z, ratio), rescale4(c.w, ratio));
       }
     }
-    const Divisor by(s);
     uint2* to = reinterpret_cast<uint2*>(pages + base);
+    const float inv = pow2_reciprocal(s);
+    if (finite && inv > 0.f) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = quantise8(v[i], by);
+      for (int i = 0; i < VPT; ++i)
+        if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = quantise8(v[i], inv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = quantise8_any(v[i], s);
+    }
     if (t == 0) *scale = s;
   }
 }
@@ -221,11 +263,14 @@ __global__ void __launch_bounds__(WPI > 8 ? WPI * 32 : 256) append_kernel(const 
 // ================================================================ bookkeeping
 
 // reserve and compact put the pages in order, which takes prefix sums over all
-// of refs: one cluster of 8 blocks does that in one launch, each block a
-// consecutive range of the pages, the ranges' totals exchanged through
-// distributed shared memory.
+// of refs: one launch of one block, or, above kOneBlockPages pages, of a
+// cluster of 8, each block a consecutive range of the pages, the ranges' totals
+// exchanged through distributed shared memory (16 sequences, 1100 pages:
+// 13.3 us in a cluster that kept its lists in global memory).
 constexpr int kCluster = 8;
 constexpr int kBookThreads = 1024;
+constexpr int kOneBlockPages = 16384;
+constexpr int kSharedSeqs = 1024;  // sequences whose lists stay in shared memory
 
 __device__ __forceinline__ int page_free(int refs) { return refs <= 0 ? 1 : 0; }
 
@@ -234,6 +279,7 @@ template <class T>
 __device__ __forceinline__ T block_scan(T x, T* warp_sums, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   T inc = x;
+#pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
     const T y = __shfl_up_sync(0xffffffffu, inc, i);
     if (lane >= i) inc += y;
@@ -241,14 +287,16 @@ __device__ __forceinline__ T block_scan(T x, T* warp_sums, T* total) {
   __syncthreads();  // warp_sums may still be read from the scan before
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  T before = 0, all = 0;
-  for (int i = 0; i < kBookThreads / 32; ++i) {
-    const T y = warp_sums[i];
-    if (i < warp) before += y;
-    all += y;
+  static_assert(kBookThreads == 1024, "a lane for each warp's sum");
+  T s = warp_sums[lane];
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, s, i);
+    if (lane >= i) s += y;
   }
-  *total = all;
-  return before + inc - x;
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  const T before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0) + inc - x;
 }
 
 __device__ __forceinline__ int ld_dsmem_int(const int* p, int rank) {
@@ -258,28 +306,41 @@ __device__ __forceinline__ int ld_dsmem_int(const int* p, int rank) {
 }
 
 // This block's range of the pages: consecutive, a multiple of the block's step.
+template <int CL>
 __device__ __forceinline__ void page_range(int num_pages, int* first, int* last) {
   const long long step = kBookThreads;
-  const long long per = ((num_pages + kCluster - 1ll) / kCluster + step - 1) / step * step;
-  *first = static_cast<int>(min(per * cluster_ctarank(), static_cast<long long>(num_pages)));
-  *last = static_cast<int>(min(per * (cluster_ctarank() + 1ll), static_cast<long long>(num_pages)));
+  const long long per = ((num_pages + CL - 1ll) / CL + step - 1) / step * step;
+  *first = static_cast<int>(min(per * blockIdx.x, static_cast<long long>(num_pages)));
+  *last = static_cast<int>(min(per * (blockIdx.x + 1ll), static_cast<long long>(num_pages)));
+}
+
+template <int CL>
+__device__ __forceinline__ void book_sync() {
+  if constexpr (CL > 1) cluster_sync_all();
+  else __syncthreads();
 }
 
 // Counts the pages of the range for which `want` holds, and gives the number
 // of such pages in the ranges before this one and in all of them.
-template <class F>
+template <int CL, class F>
 __device__ __forceinline__ void count_pages(int first, int last, int* mine, int* warp_sums, F want, int* before,
                                             int* all) {
   int n = 0;
+#pragma unroll 4
   for (int p = first + static_cast<int>(threadIdx.x); p < last; p += kBookThreads) n += want(p);
   int total;
   block_scan(n, warp_sums, &total);
+  if constexpr (CL == 1) {
+    *before = 0;
+    *all = total;
+    return;
+  }
   if (threadIdx.x == 0) *mine = total;
   cluster_sync_all();
   int b = 0, t = 0;
-  for (int r = 0; r < kCluster; ++r) {
+  for (int r = 0; r < CL; ++r) {
     const int y = ld_dsmem_int(mine, r);
-    if (r < static_cast<int>(cluster_ctarank())) b += y;
+    if (r < static_cast<int>(blockIdx.x)) b += y;
     t += y;
   }
   *before = b;
@@ -292,17 +353,28 @@ __device__ __forceinline__ void count_pages(int first, int last, int* mine, int*
 //   copy:  number of the move, or -1
 //   from:  the shared page
 // header[0]: pages handed out in all.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
+template <int CL>
+__global__ void __launch_bounds__(kBookThreads)
     reserve_kernel(int* table, int* lens, int* refs, const int* grow, int* granted, int* moves, int* ws, int B,
                    int max_pages, int num_pages, int P) {
-  __shared__ int mine, warp_sums[kBookThreads / 32];
+  __shared__ int mine, warp_sums[kBookThreads / 32], taken_sh;
   __shared__ long long warp_sums64[kBookThreads / 32];
+  __shared__ int lists[4 * kSharedSeqs];
   const int tid = threadIdx.x;
+  begin_kernel();
+  const bool small = B <= kSharedSeqs;
   int *begin = ws + kPagesHeader, *have = begin + B, *copy = have + B, *from = copy + B;
+  if (CL == 1 && small) begin = lists, have = begin + B, copy = have + B, from = copy + B;
   int first, last, before, free_all;
-  page_range(num_pages, &first, &last);
-  count_pages(first, last, &mine, warp_sums, [&](int p) { return page_free(refs[p]); }, &before, &free_all);
-  if (cluster_ctarank() == 0) {
+  page_range<CL>(num_pages, &first, &last);
+  // what the first chunk of sequences needs is asked for before the pages are counted
+  int old0 = 0, grow0 = 0;
+  if (blockIdx.x == 0 && tid < B) {
+    old0 = lens[tid];
+    grow0 = grow ? grow[tid] : 1;
+  }
+  count_pages<CL>(first, last, &mine, warp_sums, [&](int p) { return page_free(refs[p]); }, &before, &free_all);
+  if (blockIdx.x == 0) {
     long long upto = 0;  // pages needed by the sequences before this chunk
     int taken = 0, copies = 0;
     for (int b0 = 0; b0 < B; b0 += kBookThreads) {
@@ -310,8 +382,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
       int old = 0, n = 0, held = 0, src = -1, shared = 0, fits = 1;
       long long need = 0;
       if (b < B) {
-        old = max(lens[b], 0);
-        n = grow ? max(grow[b], 0) : 1;
+        old = max(b0 == 0 ? old0 : lens[b], 0);
+        n = max(b0 == 0 ? grow0 : grow ? grow[b] : 1, 0);
         held = old / P + (old % P != 0);
         const long long want = (static_cast<long long>(old) + n + P - 1) / P;
         if (n > 0 && (want > max_pages || held > max_pages)) {
@@ -330,9 +402,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
       long long chunk;
       const long long at = upto + block_scan(need, warp_sums64, &chunk);
       const bool given = n > 0 && fits && (need == 0 || at + need <= free_all);
-      int chunk_copies, chunk_taken;
-      const int move = copies + block_scan(given && shared ? 1 : 0, warp_sums, &chunk_copies);
-      block_scan(given ? static_cast<int>(need) : 0, warp_sums, &chunk_taken);
+      // moves and pages of the granted in one scan: at most 1024 moves and 2^31 pages
+      long long both;
+      const long long mark = block_scan(given ? (need << 16) + shared : 0ll, warp_sums64, &both);
+      const int move = copies + static_cast<int>(mark & 0xffff);
       if (b < B) {
         begin[b] = static_cast<int>(min(at, static_cast<long long>(num_pages)));
         have[b] = held;
@@ -343,17 +416,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
         else if (n > 0) atomicOr(&g_device_error, FD_DEVERR_PAGES_EXHAUSTED);
       }
       upto += chunk;
-      taken += chunk_taken;
-      copies += chunk_copies;
+      taken += static_cast<int>(both >> 16);
+      copies += static_cast<int>(both & 0xffff);
     }
     if (tid == 0) {
-      ws[0] = taken;
+      taken_sh = ws[0] = taken;
       moves[0] = copies;
       moves[1] = free_all - taken;
     }
   }
-  cluster_sync_all();
-  const int taken = __ldcg(ws);
+  book_sync<CL>();
+  const int taken = CL == 1 ? taken_sh : __ldcg(ws);
+  if (CL > 1 && small) {
+    for (int i = tid; i < 4 * B; i += kBookThreads) lists[i] = __ldcg(begin + i);
+    begin = lists, have = begin + B, copy = have + B, from = copy + B;
+    __syncthreads();
+  }
   // the free page of rank r goes to the last sequence with begin <= r
   for (int p0 = first; p0 < last && before < taken; p0 += kBookThreads) {
     const int p = p0 + tid;
@@ -364,13 +442,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
       int lo = 0, hi = B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldcg(begin + mid) <= r) lo = mid;
+        if (begin[mid] <= r) lo = mid;
         else hi = mid;
       }
-      const int j = r - __ldcg(begin + lo), c = __ldcg(copy + lo), h = __ldcg(have + lo);
+      const int j = r - begin[lo], c = copy[lo], h = have[lo];
       if (c >= 0 && j == 0) {
         table[static_cast<size_t>(lo) * max_pages + h - 1] = p;
-        moves[2 + 2 * static_cast<size_t>(c)] = __ldcg(from + lo);
+        moves[2 + 2 * static_cast<size_t>(c)] = from[lo];
         moves[3 + 2 * static_cast<size_t>(c)] = p;
       } else {
         table[static_cast<size_t>(lo) * max_pages + h + j - (c >= 0)] = p;
@@ -379,8 +457,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
     }
     before += total;
   }
-  cluster_sync_all();  // every block has read refs: now the copied pages lose their rows
-  if (cluster_ctarank() == 0)
+  book_sync<CL>();  // every block has read refs: now the copied pages lose their rows
+  if (blockIdx.x == 0)
     for (int b = tid; b < B; b += kBookThreads)
       if (copy[b] >= 0) atomicSub(refs + from[b], 1);
 }
@@ -389,13 +467,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
 // pages in use. With r = pages in use before page p: a free page p < n is hole
 // p - r, and a page in use p >= n is mover r - (pages in use below n).
 // ws[r] = p for those movers and ws[p] = r (distinct places, as r < n <= p).
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
-    compact_kernel(int* refs, int* moves, int* ws, int num_pages) {
+template <int CL>
+__global__ void __launch_bounds__(kBookThreads) compact_kernel(int* refs, int* moves, int* ws, int num_pages) {
   __shared__ int mine, holes, warp_sums[kBookThreads / 32];
   const int tid = threadIdx.x;
+  begin_kernel();
   int first, last, before, n;
-  page_range(num_pages, &first, &last);
-  count_pages(first, last, &mine, warp_sums, [&](int p) { return 1 - page_free(refs[p]); }, &before, &n);
+  page_range<CL>(num_pages, &first, &last);
+  count_pages<CL>(first, last, &mine, warp_sums, [&](int p) { return 1 - page_free(refs[p]); }, &before, &n);
   int my_holes = 0;
   for (int p0 = first; p0 < last; p0 += kBookThreads) {
     const int p = p0 + tid;
@@ -412,24 +491,28 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBookThreads)
     }
     before += total;
   }
-  int total;
-  block_scan(my_holes, warp_sums, &total);
-  if (tid == 0) holes = total;
-  cluster_sync_all();
-  int moved = 0;
-  for (int r = 0; r < kCluster; ++r) moved += ld_dsmem_int(&holes, r);
+  int moved;
+  block_scan(my_holes, warp_sums, &moved);
+  if constexpr (CL > 1) {
+    if (tid == 0) holes = moved;
+    cluster_sync_all();
+    moved = 0;
+    for (int r = 0; r < CL; ++r) moved += ld_dsmem_int(&holes, r);
+  } else {
+    __syncthreads();
+  }
   const int below = n - moved;  // pages in use below n
-  for (int i = cluster_ctarank() * kBookThreads + tid; i < moved; i += kCluster * kBookThreads) {
+  for (int i = blockIdx.x * kBookThreads + tid; i < moved; i += CL * kBookThreads) {
     const int src = __ldcg(ws + below + i), dst = __ldcg(moves + 3 + 2 * static_cast<size_t>(i));
     moves[2 + 2 * static_cast<size_t>(i)] = src;
     refs[dst] = refs[src];
     refs[src] = 0;
   }
-  if (cluster_ctarank() == 0 && tid == 0) {
+  if (blockIdx.x == 0 && tid == 0) {
     moves[0] = moved;
     moves[1] = num_pages - n;
   }
-  cluster_sync_all();  // no block leaves while another reads its shared memory
+  if constexpr (CL > 1) cluster_sync_all();  // no block leaves while another reads its shared memory
 }
 
 constexpr int kTableThreads = 256;
@@ -437,6 +520,7 @@ constexpr int kTableThreads = 256;
 // Table entries follow the moves of compact_kernel.
 __global__ void __launch_bounds__(kTableThreads)
     renumber_kernel(int* table, const int* moves, const int* ws, long long entries, int num_pages) {
+  begin_kernel();
   const int n = num_pages - moves[1], below = n - moves[0];
   for (long long i = blockIdx.x * static_cast<long long>(kTableThreads) + threadIdx.x; i < entries;
        i += static_cast<long long>(gridDim.x) * kTableThreads) {
@@ -457,6 +541,7 @@ __global__ void __launch_bounds__(kTableThreads)
 __global__ void __launch_bounds__(kTableThreads)
     fork_kernel(const int* table, const int* lens, const int* parent, int* table_out, int* lens_out, int* refs, int B,
                 int B_out, int max_pages, int num_pages) {
+  begin_kernel();
   const int i = blockIdx.y;  // a row: old, new or both
   int from = -1;
   if (i < B_out) {
@@ -492,6 +577,7 @@ __global__ void __launch_bounds__(kTableThreads)
 
 __global__ void __launch_bounds__(kTableThreads)
     free_kernel(int* table, int* lens, int* refs, const int* keep, int window, int max_pages, int num_pages, int P) {
+  begin_kernel();
   const int b = blockIdx.y;
   // every thread of the row takes this minimum, before or after it is stored
   const int len = max(*static_cast<volatile int*>(lens + b), 0);
@@ -520,6 +606,7 @@ constexpr size_t kCopyPiece = static_cast<size_t>(kCopyThreads) * kCopyVecs * 16
 __global__ void __launch_bounds__(kCopyThreads)
     copy_kernel(uint4* k, uint4* v, float* ks, float* vs, const int* moves, int room, int layers, int num_pages,
                 int NKV, size_t page_vecs, int pieces) {
+  begin_kernel();
   const int n = min(max(moves[0], 0), room);
   const long long items = static_cast<long long>(n) * layers * 2 * pieces;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
@@ -552,15 +639,30 @@ __global__ void __launch_bounds__(kCopyThreads)
   }
 }
 
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int block, int cluster, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 int row_blocks(int max_pages) { return std::min((max_pages + kTableThreads - 1) / kTableThreads, 64); }
 
 template <bool KV8, int VPT, int WPI>
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   constexpr int kBlock = WPI > 8 ? WPI * 32 : 256, kItems = kBlock / 32 / WPI;
   const long long units = a.start ? static_cast<long long>(a.T) / a.P + 2ll * a.B : a.B;
-  append_kernel<KV8, VPT, WPI>
-      <<<dim3(static_cast<unsigned>(units), (2 * a.NKV + kItems - 1) / kItems), kBlock, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch(append_kernel<KV8, VPT, WPI>, dim3(static_cast<unsigned>(units), (2 * a.NKV + kItems - 1) / kItems),
+                kBlock, 1, stream, a);
 }
 
 // Warps of an item: as many as hold a page's tokens of one head in 8 vectors a
@@ -587,34 +689,32 @@ cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_pages_reserve(int* table, int* lens, int* refs, const int* grow, int* granted, int* moves, int* ws,
                                  int B, int max_pages, int num_pages, int P, cudaStream_t stream) {
-  reserve_kernel<<<kCluster, kBookThreads, 0, stream>>>(table, lens, refs, grow, granted, moves, ws, B, max_pages,
-                                                        num_pages, P);
-  return cudaGetLastError();
+  const bool one = num_pages <= kOneBlockPages;
+  return launch(one ? reserve_kernel<1> : reserve_kernel<kCluster>, dim3(one ? 1 : kCluster), kBookThreads,
+                one ? 1 : kCluster, stream, table, lens, refs, grow, granted, moves, ws, B, max_pages, num_pages, P);
 }
 
 cudaError_t launch_pages_fork(const int* table, const int* lens, const int* parent, int* table_out, int* lens_out,
                               int* refs, int B, int B_out, int max_pages, int num_pages, cudaStream_t stream) {
-  fork_kernel<<<dim3(row_blocks(max_pages), std::max(B, B_out)), kTableThreads, 0, stream>>>(
-      table, lens, parent, table_out, lens_out, refs, B, B_out, max_pages, num_pages);
-  return cudaGetLastError();
+  return launch(fork_kernel, dim3(row_blocks(max_pages), std::max(B, B_out)), kTableThreads, 1, stream, table, lens,
+                parent, table_out, lens_out, refs, B, B_out, max_pages, num_pages);
 }
 
 cudaError_t launch_pages_free(int* table, int* lens, int* refs, const int* keep, int window, int B, int max_pages,
                               int num_pages, int P, cudaStream_t stream) {
-  free_kernel<<<dim3(row_blocks(max_pages), B), kTableThreads, 0, stream>>>(table, lens, refs, keep, window, max_pages,
-                                                                            num_pages, P);
-  return cudaGetLastError();
+  return launch(free_kernel, dim3(row_blocks(max_pages), B), kTableThreads, 1, stream, table, lens, refs, keep, window,
+                max_pages, num_pages, P);
 }
 
 cudaError_t launch_pages_compact(int* table, int* refs, int* moves, int* ws, int B, int max_pages, int num_pages,
                                  cudaStream_t stream) {
-  compact_kernel<<<kCluster, kBookThreads, 0, stream>>>(refs, moves, ws, num_pages);
-  cudaError_t e = cudaGetLastError();
+  const bool one = num_pages <= kOneBlockPages;
+  const cudaError_t e = launch(one ? compact_kernel<1> : compact_kernel<kCluster>, dim3(one ? 1 : kCluster), kBookThreads,
+                               one ? 1 : kCluster, stream, refs, moves, ws, num_pages);
   const long long entries = static_cast<long long>(B) * max_pages;
   if (e != cudaSuccess || entries == 0) return e;
   const unsigned blocks = static_cast<unsigned>(std::min((entries + kTableThreads - 1) / kTableThreads, 152ll * 8));
-  renumber_kernel<<<blocks, kTableThreads, 0, stream>>>(table, moves, ws, entries, num_pages);
-  return cudaGetLastError();
+  return launch(renumber_kernel, dim3(blocks), kTableThreads, 1, stream, table, moves, ws, entries, num_pages);
 }
 
 cudaError_t launch_pages_copy(void* k, void* v, float* ks, float* vs, const int* moves, int room, int layers,
@@ -622,9 +722,8 @@ cudaError_t launch_pages_copy(void* k, void* v, float* ks, float* vs, const int*
   const int pieces = static_cast<int>((page_bytes + kCopyPiece - 1) / kCopyPiece);
   const long long items = static_cast<long long>(room) * layers * 2 * pieces;
   const unsigned blocks = static_cast<unsigned>(std::min(items, 152ll * 8));
-  copy_kernel<<<blocks, kCopyThreads, 0, stream>>>(static_cast<uint4*>(k), static_cast<uint4*>(v), ks, vs, moves, room,
-                                                   layers, num_pages, NKV, page_bytes / 16, pieces);
-  return cudaGetLastError();
+  return launch(copy_kernel, dim3(blocks), kCopyThreads, 1, stream, static_cast<uint4*>(k), static_cast<uint4*>(v), ks,
+                vs, moves, room, layers, num_pages, NKV, page_bytes / 16, pieces);
 }
 
 cudaError_t read_and_clear_device_error_pages(unsigned int* err) {
