@@ -33,6 +33,9 @@ int check_shape(int B, int NH, int NKV, int HS, int page_size, int max_pages, in
   if (!supported_hs(HS) || !supported_page(page_size)) return FD_ERR_UNSUPPORTED;
   if (NH % NKV != 0 || NH / NKV > kMaxGroup) return FD_ERR_UNSUPPORTED;
   if (static_cast<long long>(max_pages) * page_size > kMaxPositions) return FD_ERR_UNSUPPORTED;  // lens are int32
+  // the kernels count the 32-position granules of one head, and 64 KB of them more for each sequence, in 32 bits
+  if (static_cast<long long>(B) * (static_cast<long long>(max_pages) * page_size / 32 + 32) > INT_MAX)
+    return FD_ERR_UNSUPPORTED;
   return FD_OK;
 }
 

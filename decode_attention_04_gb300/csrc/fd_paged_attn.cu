@@ -538,48 +538,51 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     }
   };
   if (a.B <= kWarpSeqs) {
-    // every warp by itself, without a barrier: a lane takes four sequences
-    int x[4], before[4];
-    long long mine = 0;  // 2^26 granules at most in each
+    // Every warp by itself, without a barrier, 32 sequences a turn (a turn is
+    // little code: fetching it is most of what it costs). A head's places are
+    // below 2^31 (checked on the host).
     unsigned flags = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int b = 4 * lane + k;
+    int sum = 0, x = 0, upto = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane;
       const int raw_len = b < a.B ? a.lens[b] : 0, len = clamp_len(a, raw_len);
       if (raw_len < 0) flags |= FD_DEVERR_LEN_NEGATIVE;
       if (raw_len > len) flags |= FD_DEVERR_LEN_CLAMPED;
       if (b < a.B) lens[b] = len;  // each warp writes the same, and reads its own
-      x[k] = places(a, band_from(a, len));
-      before[k] = static_cast<int>(mine);
-      mine += x[k];
+      x = places(a, band_from(a, len));
+      upto = x;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, i);
+        if (lane >= i) upto += y;
+      }
+      upto += sum;
+      sum = __shfl_sync(0xffffffffu, upto, 31);
     }
     if (c == 0 && warp == 0 && flags) atomicOr(&g_device_error, flags);
-    long long upto = mine;
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, i);
-      if (lane >= i) upto += y;
-    }
-    shares(__shfl_sync(0xffffffffu, upto, 31));
-    int found = -1;
-    long long off = 0;
-    int gran = 1;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const long long o = (upto - mine + before[k]) * a.NKV;
-      if (x[k] > 0 && o <= per * c && per * c < o + static_cast<long long>(x[k]) * a.NKV) {
-        found = 4 * lane + k;
-        off = o;
-        gran = x[k];
+    shares(sum);
+    // the sequence that holds the share's first place, from the last turn backwards
+    const long long start = per * c;
+#pragma unroll 1
+    for (int b0 = (a.B - 1) & ~31; walk.left > 0; b0 -= 32) {
+      const long long off = static_cast<long long>(upto - x) * a.NKV;
+      const unsigned who = __ballot_sync(0xffffffffu, x > 0 && off <= start);
+      if (who) {  // the last one that begins at or before it
+        const int src = 31 - __clz(who);
+        begin_at(b0 + src, __shfl_sync(0xffffffffu, off, src), __shfl_sync(0xffffffffu, x, src));
+        break;
       }
-    }
-    const unsigned who = __ballot_sync(0xffffffffu, found >= 0);
-    if (who) {
-      const int src = __ffs(who) - 1;
-      found = __shfl_sync(0xffffffffu, found, src);
-      off = __shfl_sync(0xffffffffu, off, src);
-      gran = __shfl_sync(0xffffffffu, gran, src);
-      begin_at(found, off, gran);
+      // a turn earlier: its places end where this one's begin
+      const int end = __shfl_sync(0xffffffffu, upto - x, 0);
+      x = places(a, band_from(a, lens[b0 - 32 + lane]));
+      upto = x;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, i);
+        if (lane >= i) upto += y;
+      }
+      upto += end - __shfl_sync(0xffffffffu, upto, 31);
     }
     __syncwarp();
   } else {
@@ -940,19 +943,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     float2* stat = reinterpret_cast<float2*>(red + 2 * 11 * C::NQ);
     const uint32_t o_cols = tmem + tlane + C::O_COL;
 
-    stage_q(walk.t, tid - W_SOFT0 * 32, 2 * kSoft);
-    named_bar_sync(BAR_BOTH, 2 * kSoft);
-    if (grp == 0 && tq == 0) mbar_arrive(q_ready);
-
-    // This group's tiles: the current one and the next.
+    // This group's tiles: the current one and the next. The look-ups are in
+    // flight while the first segment's query rows are brought.
+    const Tile first_tile = walk.t;
     if (grp == 1) next_tile(a, lens, walk);
     Tile cur = walk.t;
     int page = entry(cur);
+    stage_q(first_tile, tid - W_SOFT0 * 32, 2 * kSoft);
+    float2 ksvs = scales(cur, page);
+    named_bar_sync(BAR_BOTH, 2 * kSoft);
+    if (grp == 0 && tq == 0) mbar_arrive(q_ready);
     next_tile(a, lens, walk);
     next_tile(a, lens, walk);
     Tile nxt = walk.t;
     int next_page = entry(nxt);
-    float2 ksvs = scales(cur, page);
     // Per row: the reference (the running maximum less the bias), this thread's share of the sum. A lane
     // also keeps the reference of the row that it ends with in a row reduction.
     constexpr float kNone = -3e38f;  // below every score

@@ -46,7 +46,7 @@ def _attn(**kw):
     (dict(N=0), fd.FD_ERR_INVALID_ARG), (dict(HS=96), fd.FD_ERR_UNSUPPORTED), (dict(HS=1024), fd.FD_ERR_UNSUPPORTED),
     (dict(P=8), fd.FD_ERR_UNSUPPORTED), (dict(P=48), fd.FD_ERR_UNSUPPORTED), (dict(P=256), fd.FD_ERR_UNSUPPORTED),
     (dict(NH=9), fd.FD_ERR_UNSUPPORTED), (dict(NH=34), fd.FD_ERR_UNSUPPORTED),
-    (dict(mp=1 << 27), fd.FD_ERR_UNSUPPORTED),
+    (dict(mp=1 << 27), fd.FD_ERR_UNSUPPORTED), (dict(B=65535, mp=1 << 16), fd.FD_ERR_UNSUPPORTED),
     *[({n: None}, fd.FD_ERR_INVALID_ARG) for n in ("q", "k", "v", "ks", "vs", "out", "table", "lens")],
 ])
 def test_attn_refuses(kw, want):
