@@ -1044,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           tc_fence_after();
 #pragma unroll 1
           for (int x = 0; x < C::NB * C::NP; x += 16) {
-            // 16 columns: of NQ = 16 rows one term, of fewer rows several
+              // 16 columns: of NQ = 16 rows one term, of fewer rows several
             float o[16];
             tmem_load<16>(o_cols + C::NP * C::NB * grp + x, o);
 #pragma unroll
@@ -1156,23 +1156,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           float x[C::NQ];
 #pragma unroll
           for (int r = 0; r < C::NQ; ++r) x[r] = 0.f;
-          // the groups' accumulators, and their terms, in fixed order
-          constexpr int kLoads = C::NQ == 16 ? C::PT : 1;
+          // the groups' accumulators, and their terms, in fixed order, 16 columns at a time
+          constexpr int kLoads = C::NP / 16, kTerms = 16 / C::NQ;
 #pragma unroll 1
           for (int n = both ? 0 : grp * kLoads; n < (both ? 2 : grp + 1) * kLoads; ++n) {
-            const int k = n / kLoads, term = n % kLoads;
+            const int k = n / kLoads, part_no = n % kLoads;
             float o[16];
-            tmem_load<16>(o_cols + C::NP * (C::NB * k + mb) + 16 * term, o);
-            if constexpr (C::NQ == 16) {
+            tmem_load<16>(o_cols + C::NP * (C::NB * k + mb) + 16 * part_no, o);
+#pragma unroll
+            for (int j = 0; j < kTerms; ++j) {
+              const int term = part_no * kTerms + j;
+              if (term >= C::PT) break;  // columns of no term hold anything
               const float by = !C::KV8 || term == 0 ? 1.f : term == 1 ? 0.0625f : 0.00390625f;
 #pragma unroll
-              for (int r = 0; r < 16; ++r) x[r] += fac[k * C::NQ + r] * by * o[r];
-            } else {
-#pragma unroll
-              for (int r = 0; r < C::NQ; ++r)
-                x[r] += fac[k * C::NQ + r] *
-                        (C::KV8 ? o[r] + (o[C::NQ + r] + o[(C::PT - 1) * C::NQ + r] * 0.0625f) * 0.0625f
-                                : o[r] + o[C::NQ + r]);
+              for (int r = 0; r < C::NQ; ++r) x[r] += fac[k * C::NQ + r] * by * o[j * C::NQ + r];
             }
           }
           const int d = mb * 128 + pl;  // O^T lanes are head dims
@@ -1387,7 +1384,11 @@ cudaError_t launch_cfg(const PagedArgs& a, cudaStream_t stream) {
 
 template <int HS, bool KV8>
 cudaError_t launch_group(const PagedArgs& a, cudaStream_t stream) {
-  return a.NH / a.NKV <= 4 ? launch_cfg<Cfg<HS, KV8, 4>>(a, stream) : launch_cfg<Cfg<HS, KV8, 16>>(a, stream);
+  // the rows that a softmax thread works on: 4, 8 or 16, as the group has
+  const int G = a.NH / a.NKV;
+  if (G <= 4) return launch_cfg<Cfg<HS, KV8, 4>>(a, stream);
+  if (G <= 8) return launch_cfg<Cfg<HS, KV8, 8>>(a, stream);
+  return launch_cfg<Cfg<HS, KV8, 16>>(a, stream);
 }
 
 template <bool KV8>
