@@ -1271,16 +1271,28 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     }
     if (base == i0) {
       for (int q = r0 + warp; q <= r1; q += kMergeThreads / 32) {
+        // a lane's parts in registers, read once (more than 256 parts: the rest twice)
+        constexpr int kHeld = 8;
+        float2 y[kHeld];
         float m = kNegInf;  // every part has a finite reference
-        for (int p = lane; p < parts; p += 32) m = fmaxf(m, ml[static_cast<size_t>(slot_of(p)) * G + q].x);
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+          const int p = lane + 32 * j;
+          y[j] = p < parts ? ml[static_cast<size_t>(slot_of(p)) * G + q] : make_float2(kNegInf, 0.f);
+          m = fmaxf(m, y[j].x);
+        }
+        for (int p = lane + 32 * kHeld; p < parts; p += 32) m = fmaxf(m, ml[static_cast<size_t>(slot_of(p)) * G + q].x);
         for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
         float l = 0.f;
-        for (int p = lane; p < parts; p += 32) {
-          const float2 y = ml[static_cast<size_t>(slot_of(p)) * G + q];
-          const float f = exp2f(y.x - m);
+        auto one = [&](int p, const float2& v) {
+          const float f = exp2f(v.x - m);
           factor[(q - r0) * parts + p] = f;
-          l += f * y.y;
-        }
+          l += f * v.y;
+        };
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+          if (lane + 32 * j < parts) one(lane + 32 * j, y[j]);
+        for (int p = lane + 32 * kHeld; p < parts; p += 32) one(p, ml[static_cast<size_t>(slot_of(p)) * G + q]);
         for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
         if (lane == 0) inv[q] = l == 0.f ? 0.f : 1.f / l;
       }
@@ -1305,7 +1317,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     }
     __syncthreads();
     if (g == 0) {
-      for (int j = 1; j < groups && j < parts; ++j) add(acc[j * n + tid], 1.f);
+#pragma unroll 4
+      for (int j = 1; j < min(groups, parts); ++j) add(acc[j * n + tid], 1.f);
       const float by = inv[r];
       const float4 y = make_float4(s.x * by, s.y * by, s.z * by, s.w * by);
       const size_t at = (static_cast<size_t>(cut.b) * a.NH + static_cast<size_t>(cut.kvh) * G + r) * a.HS + 4 * d;
