@@ -179,7 +179,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
 // once. A block looks its unit up once for BLOCK / (32 WPI) items.
 // Bound by memory: 2 bytes in and 1 out an element.
 template <bool KV8, int VPT, int WPI>
-__global__ void __launch_bounds__(WPI > 8 ? WPI * 32 : 256) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(WPI > 8 ? WPI * 32 : 256, WPI > 16 ? 2 : WPI > 8 ? 3 : 4) append_kernel(const AppendArgs a) {
   constexpr int kBlock = WPI > 8 ? WPI * 32 : 256;
   constexpr int kItems = kBlock / 32 / WPI;
   __shared__ uint32_t red[kBlock / 32];
@@ -187,76 +187,79 @@ __global__ void __launch_bounds__(WPI > 8 ? WPI * 32 : 256) append_kernel(const 
   begin_kernel();
   const Segment g = find_segment(a, blockIdx.x, lane, blockIdx.y == 0 && tid == 0);
   if (g.n <= 0) return;
-  const int item = blockIdx.y * kItems + tid / (32 * WPI);
-  const bool there = item < 2 * a.NKV;
-  const int w = item & 1, head = item >> 1, t = tid % (32 * WPI);
+  const int t = tid % (32 * WPI);
   const int row_shift = 28 - __clz(a.HS);  // vectors of a row: HS / 8
-  const int vecs = there ? g.n << row_shift : 0;
-  const long long stride = w ? a.stride[1] : a.stride[0];
-  const uint16_t* x = (w ? a.x[1] : a.x[0]) + g.row * stride + static_cast<size_t>(head) * a.HS;
-  uint4 v[VPT];
+  for (int item0 = blockIdx.y * kItems; item0 < 2 * a.NKV; item0 += gridDim.y * kItems) {
+    const int item = item0 + tid / (32 * WPI);
+    const bool there = item < 2 * a.NKV;
+    const int w = item & 1, head = item >> 1;
+    const int vecs = there ? g.n << row_shift : 0;
+    const long long stride = w ? a.stride[1] : a.stride[0];
+    const uint16_t* x = (w ? a.x[1] : a.x[0]) + g.row * stride + static_cast<size_t>(head) * a.HS;
+    uint4 v[VPT];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int at = t + i * 32 * WPI, row = at >> row_shift, col = at & ((1 << row_shift) - 1);
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (at < vecs) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + row * stride + col * 8));
-  }
-  const size_t block = static_cast<size_t>(g.page) * a.NKV + head;
-  const size_t base = (block * a.P + g.slot) * a.HS;
-  if constexpr (!KV8) {
-    uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(w ? a.pages[1] : a.pages[0]) + base);
+    for (int i = 0; i < VPT; ++i) {
+      const int at = t + i * 32 * WPI, row = at >> row_shift, col = at & ((1 << row_shift) - 1);
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (at < vecs) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + row * stride + col * 8));
+    }
+    const size_t block = static_cast<size_t>(g.page) * a.NKV + head;
+    const size_t base = (block * a.P + g.slot) * a.HS;
+    if constexpr (!KV8) {
+      uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(w ? a.pages[1] : a.pages[0]) + base);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = v[i];
-  } else {
-    float* scale = (w ? a.scale[1] : a.scale[0]) + block;
-    const float old = there && g.slot > 0 ? *scale : 0.f;
-    // the largest |x| by its bits, two at a time
-    uint32_t m = 0;
+      for (int i = 0; i < VPT; ++i)
+        if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = v[i];
+    } else {
+      float* scale = (w ? a.scale[1] : a.scale[0]) + block;
+      const float old = there && g.slot > 0 ? *scale : 0.f;
+      // the largest |x| by its bits, two at a time
+      uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      m = __vmaxu2(__vmaxu2(__vmaxu2(m, v[i].x & 0x7fff7fffu), __vmaxu2(v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu)),
-                   v[i].w & 0x7fff7fffu);
-    m = block_max<WPI>(max(m & 0xffffu, m >> 16), red);
-    const bool finite = m < 0x7f80u;
-    if (!finite) {  // once more, without the values that are not
-      m = 0;
+      for (int i = 0; i < VPT; ++i)
+        m = __vmaxu2(__vmaxu2(__vmaxu2(m, v[i].x & 0x7fff7fffu), __vmaxu2(v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu)),
+                     v[i].w & 0x7fff7fffu);
+      m = block_max<WPI>(max(m & 0xffffu, m >> 16), red);
+      const bool finite = m < 0x7f80u;
+      if (!finite) {  // once more, without the values that are not
+        m = 0;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (int i = 0; i < VPT; ++i) {
+          const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t abs2 = u[k] & 0x7fff7fffu;
-          m = __vmaxu2(m, abs2 & ~__vcmpgeu2(abs2, 0x7f807f80u));
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t abs2 = u[k] & 0x7fff7fffu;
+            m = __vmaxu2(m, abs2 & ~__vcmpgeu2(abs2, 0x7f807f80u));
+          }
+        }
+        m = max(m & 0xffffu, m >> 16);
+      }
+      // every warp of a block that has several items comes here if one does
+      if (WPI == 1 ? !finite : __syncthreads_or(!finite)) m = block_max<WPI>(m, red);
+      if (!there) continue;
+      const float s = fmaxf(block_scale(__uint_as_float(m << 16)), old);
+      uint8_t* pages = static_cast<uint8_t*>(w ? a.pages[1] : a.pages[0]);
+      if (g.slot > 0 && s > old) {  // the earlier tokens' codes, rounded to the new scale
+        const float ratio = old / s;
+        uint4* held = reinterpret_cast<uint4*>(pages + block * a.P * a.HS);
+        for (int i = t; i < g.slot * a.HS / 16; i += 32 * WPI) {
+          const uint4 c = held[i];
+          held[i] = make_uint4(rescale4(c.x, ratio), rescale4(c.y, ratio), rescale4(c.z, ratio), rescale4(c.w, ratio));
         }
       }
-      m = max(m & 0xffffu, m >> 16);
-    }
-    // every warp of a block that has several items comes here if one does
-    if (WPI == 1 ? !finite : __syncthreads_or(!finite)) m = block_max<WPI>(m, red);
-    if (!there) return;
-    const float s = fmaxf(block_scale(__uint_as_float(m << 16)), old);
-    uint8_t* pages = static_cast<uint8_t*>(w ? a.pages[1] : a.pages[0]);
-    if (g.slot > 0 && s > old) {  // the earlier tokens' codes, rounded to the new scale
-      const float ratio = old / s;
-      uint4* held = reinterpret_cast<uint4*>(pages + block * a.P * a.HS);
-      for (int i = t; i < g.slot * a.HS / 16; i += 32 * WPI) {
-        const uint4 c = held[i];
-        held[i] = make_uint4(rescale4(c.x, ratio), rescale4(c.y, ratio), rescale4(c.z, ratio), rescale4(c.w, ratio));
+      uint2* to = reinterpret_cast<uint2*>(pages + base);
+      const float inv = pow2_reciprocal(s);
+      if (finite && inv > 0.f) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+          if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = quantise8(v[i], inv);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+          if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = quantise8_any(v[i], s);
       }
+      if (t == 0) *scale = s;
     }
-    uint2* to = reinterpret_cast<uint2*>(pages + base);
-    const float inv = pow2_reciprocal(s);
-    if (finite && inv > 0.f) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = quantise8(v[i], inv);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (t + i * 32 * WPI < vecs) to[t + i * 32 * WPI] = quantise8_any(v[i], s);
-    }
-    if (t == 0) *scale = s;
   }
 }
 
@@ -661,8 +664,12 @@ template <bool KV8, int VPT, int WPI>
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   constexpr int kBlock = WPI > 8 ? WPI * 32 : 256, kItems = kBlock / 32 / WPI;
   const long long units = a.start ? static_cast<long long>(a.T) / a.P + 2ll * a.B : a.B;
-  return launch(append_kernel<KV8, VPT, WPI>, dim3(static_cast<unsigned>(units), (2 * a.NKV + kItems - 1) / kItems),
-                kBlock, 1, stream, a);
+  // One block for a unit's items where there are units enough: looking a unit up
+  // costs a warp as much as an item of 16 tokens (8 prompts, 8 heads: two blocks
+  // a unit 40.6 us).
+  const int rounds = (2 * a.NKV + kItems - 1) / kItems;
+  return launch(append_kernel<KV8, VPT, WPI>, dim3(static_cast<unsigned>(units), units >= 1024 ? 1 : rounds), kBlock, 1,
+                stream, a);
 }
 
 // Warps of an item: as many as hold a page's tokens of one head in 8 vectors a
