@@ -620,6 +620,16 @@ int fd_decode_attn_fp8(const void* q, const void* k8, const void* v8, const floa
                   stream);
 }
 
+}  // extern "C"
+
+namespace fd {
+
+int debug_withhold_tile() { return g_withhold_tile.load(std::memory_order_relaxed); }
+
+}  // namespace fd
+
+extern "C" {
+
 int fd_debug_withhold_copies(int withhold_tile, unsigned long long wait_limit_ns) {
   const bool on = withhold_tile >= 0;
   const unsigned long long ns = on ? wait_limit_ns : 0;

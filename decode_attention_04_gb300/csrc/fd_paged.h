@@ -26,6 +26,7 @@ struct PagedArgs {
   int B, NH, NKV, HS, P, num_pages, max_pages, window;
   int blocks, granule, min_share;
   int kv8;
+  int withhold_tile;       // test hook: a block's copy warps stop at this tile of theirs (a huge value: off)
   float scale_log2;        // scale * log2(e)
 };
 
@@ -61,6 +62,9 @@ cudaError_t launch_pages_copy(void* k, void* v, float* ks, float* vs, const int*
 cudaError_t read_and_clear_device_error_paged(unsigned int* err);
 cudaError_t read_and_clear_device_error_pages(unsigned int* err);
 cudaError_t set_wait_limit_paged(unsigned long long ns);
+
+// The test hook's tile (fd_debug_withhold_copies), INT_MAX where it is off.
+int debug_withhold_tile();
 
 // Streaming multiprocessors of a device (cached), and the library's own
 // workspace of the paged attention for (device, stream): FD_* status codes.

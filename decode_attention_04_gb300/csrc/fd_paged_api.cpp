@@ -118,6 +118,7 @@ int run(const fd_paged_plan_t& p, void* workspace, size_t workspace_bytes, float
   a.granule = p.granule;
   a.min_share = p.min_share;
   a.kv8 = kv8;
+  a.withhold_tile = fd::debug_withhold_tile();
   a.scale_log2 = scale * 1.4426950408889634f;
   return fd::launch_paged_attn(a, stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }

@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     int page = page_of(cur);
     int slot = slot0;
     uint32_t turn = 1;  // parity of `empty` that lets this turn of the ring begin: none in the first
-    while (cur.ok) {
+    for (int n = 0; cur.ok && n < a.withhold_tile; ++n) {
       next_tile(a, lens, walk);
       const Tile nxt = walk.t;
       const int next_page = page_of(nxt);  // in flight while this tile's copies wait for slots

@@ -404,7 +404,8 @@ int fd_decode_attn_noalloc(const void* q, const void* k_cache, const void* v_cac
 /*
  * fd_debug_withhold_copies: a test hook for the bounded waits (no counterpart
  * on the pages). With withhold_tile >= 0, the tensor-core split blocks of
- * every later call on any device issue no K/V copies for their tiles from
+ * every later call on any device, and the blocks of fd_paged_attn
+ * (fd_paged_attn.h), issue no K/V copies for their tiles from
  * index withhold_tile on (they never issue those copies, so nothing is left
  * in flight), the consumer warps' wait for that tile gives up after
  * wait_limit_ns nanoseconds (0: the default, about one second), the call

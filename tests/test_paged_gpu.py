@@ -305,6 +305,31 @@ def test_attn_refuses_to_allocate_during_capture():
     assert torch.isfinite(fd.paged_attention(*a, out=out).float()).all()
 
 
+@pytest.mark.parametrize("kv", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("HS,G", [(128, 4), (512, 16)])
+@pytest.mark.parametrize("tile", [0, 1])
+def test_attn_waits_are_bounded(kv, HS, G, tile):
+    """Copies that are never issued: the waits for them give up, the call returns with the error bit, and the next call is
+    right again."""
+    P, lens = 32, [900, 40, 2000]
+    N, wide = 100, 63
+    k, ks, _ = make_pool(kv, N, 1, P, HS, 3)
+    v, vs, _ = make_pool(kv, N, 1, P, HS, 4)
+    q = _values((3, G, HS), 5).bfloat16()
+    table = make_table(lens, P, wide, N, 9)
+    want, _, err = run_attn(kv, q, k, ks, v, vs, table, lens, 0)
+    assert err == 0
+    try:
+        fd.fd_debug_withhold_copies(tile, 100_000)
+        _, _, err = run_attn(kv, q, k, ks, v, vs, table, lens, 0)
+    finally:
+        fd.fd_debug_withhold_copies(-1)
+    assert err & ~fd.FD_DEVERR_WAIT_TIMEOUT == 0
+    assert err or tile > 0  # a share may have a single tile
+    got, _, err = run_attn(kv, q, k, ks, v, vs, table, lens, 0)
+    assert err == 0 and torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
 # ------------------------------------------------------------------- the writer
 
 def append_both(kv, lens, start, count, T, NKV, HS, P, table, N, seed=0, new=None, pad=0, pools=None):
