@@ -24,6 +24,18 @@ The first call for a (device, stream) sizes the library's workspace; later
 calls may be captured in a CUDA graph. fd_plan / fd_decode_attn_ex take an
 explicit plan and workspace instead (nothing allocated by the library), and
 fd_decode_attn_noalloc uses a fixed scratch array compiled into libfd.so.
+
+With a cache in pages (include/fd_paged_attn.h), one decode step of all layers:
+
+    # k_pages, v_pages: [layers, num_pages, NKV, page_size, HS] bf16, or uint8 E4M3 codes with
+    # k_scale, v_scale: fp32 [layers, num_pages, NKV]; table int32 [B, max_pages], lens [B], refs [num_pages]
+    fd.fd_pages_reserve(table, lens, refs, None, granted, moves, ws, ws.numel(), B, max_pages, num_pages, page_size)
+    fd.fd_pages_copy(k_pages, v_pages, k_scale, v_scale, moves, B, layers, num_pages, NKV, page_size, HS, fd.FD_KV_E4M3)
+    for n in range(layers):
+        # k, v: the layer's new tokens [B, NKV, HS] bf16
+        fd.fd_paged_append(k, v, k_pages[n], v_pages[n], k_scale[n], v_scale[n], table, lens, None, granted, B, B, NKV,
+                           HS, page_size, num_pages, max_pages, k.stride(0), v.stride(0), fd.FD_KV_E4M3)
+        out = fd.paged_attention(q, k_pages[n], v_pages[n], table, lens, k_scale=k_scale[n], v_scale=v_scale[n])
 """
 
 from __future__ import annotations
