@@ -24,7 +24,7 @@ struct PagedArgs {
   float* ws_ml;            // fp32 [2 * blocks][G][2]
   void* cuts;              // [blocks]: the unit that each share's end cuts
   int B, NH, NKV, HS, P, num_pages, max_pages, window;
-  int blocks, granule, min_share;
+  int blocks, min_share;
   int kv8;
   int withhold_tile;       // test hook: a block's copy warps stop at this tile of theirs (a huge value: off)
   float scale_log2;        // scale * log2(e)

@@ -54,7 +54,7 @@ int make_plan(int B, int NH, int NKV, int HS, int page_size, int max_pages, int 
   if (!plan) return FD_ERR_INVALID_ARG;
   const int rc = check_shape(B, NH, NKV, HS, page_size, max_pages, kv_dtype);
   if (rc != FD_OK) return rc;
-  if (num_sms <= 0) return FD_ERR_INVALID_ARG;
+  if (num_sms <= 0 || num_sms > 1024) return FD_ERR_INVALID_ARG;  // the merge keeps 2 factors a block in shared memory
   fd_paged_plan_t p{};
   p.blocks = num_sms;
   p.granule = 32;
@@ -115,7 +115,6 @@ int run(const fd_paged_plan_t& p, void* workspace, size_t workspace_bytes, float
   a.max_pages = p.max_pages;
   a.window = p.window;
   a.blocks = p.blocks;
-  a.granule = p.granule;
   a.min_share = p.min_share;
   a.kv8 = kv8;
   a.withhold_tile = fd::debug_withhold_tile();

@@ -229,7 +229,7 @@ __device__ __forceinline__ void regs_inc() {
 // ------------------------------------------------------------- the division of work
 
 constexpr int kTile = 128;      // positions per tile: the M of the score MMA
-constexpr int kGranule = 32;    // positions
+constexpr int kGranule = 32;    // positions; the plan's granule
 constexpr int kLenCache = 1024; // lengths kept in shared memory when there are no more sequences
 constexpr int kWarpSeqs = 128;  // a warp finds its share by itself when there are no more sequences
 

@@ -29,7 +29,6 @@ __device__ __forceinline__ void begin_kernel() {
 
 // Tokens of one sequence that fall into one page.
 struct Segment {
-  int b;        // sequence
   int row;      // first row of k_new / v_new
   int n;        // tokens
   int slot;     // first slot that is written
@@ -41,7 +40,7 @@ struct Segment {
 // `count` the rows behind the first count[b] are left out, and lens[b] counts
 // what was granted. Rows outside [0, T) and negative positions are left out.
 __device__ __forceinline__ Segment segment_of(const AppendArgs& a, int b, int seg, bool report) {
-  Segment s{b, 0, 0, 0, -1};
+  Segment s{0, 0, 0, -1};
   long long r0 = b, n = 1;
   if (a.start) {
     r0 = a.start[b];
@@ -101,7 +100,7 @@ __device__ __forceinline__ Segment find_segment(const AppendArgs& a, long long u
   if (!a.start) return segment_of(a, static_cast<int>(unit), 0, report);
   const int b = sequence_of(a, unit, lane);
   const long long seg = unit - first_unit(a, b);
-  if (seg < 0 || seg > 0x3fffffff) return Segment{b, 0, 0, 0, -1};
+  if (seg < 0 || seg > 0x3fffffff) return Segment{0, 0, 0, -1};
   return segment_of(a, b, static_cast<int>(seg), report);
 }
 

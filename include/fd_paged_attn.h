@@ -76,7 +76,7 @@ typedef struct {
 /*
  * fd_paged_plan: plan for the given shape on CUDA device `device`; a pure host
  * computation plus device attribute queries. fd_paged_plan_sms: the same for a
- * GPU of num_sms SMs, without touching a device.
+ * GPU of num_sms (at most 1024) SMs, without touching a device.
  * Errors: FD_ERR_INVALID_ARG, FD_ERR_UNSUPPORTED, FD_ERR_CUDA.
  */
 int fd_paged_plan(int B, int NH, int NKV, int HS, int page_size, int max_pages, int window, int device,
@@ -94,7 +94,9 @@ int fd_paged_plan_sms(int B, int NH, int NKV, int HS, int page_size, int max_pag
  * [B][NH][HS], lens int32 [B]. scale <= 0 selects 1/sqrt(HS). A sequence of
  * length 0 gives a zero row. Only slots of the live band take part: what the
  * other slots of a page hold (NaN, say) has no effect, and pages outside the
- * band are not read, so their table entries may be -1.
+ * band are not read, so their table entries may be -1. An infinity in a live V
+ * gives NaN (the terms below add it times 0). A row of which no score is above
+ * -infinity is zero.
  * An entry that names no page raises FD_DEVERR_PAGE_ID and its positions are
  * left out; len_b < 0 counts as 0 (FD_DEVERR_LEN_NEGATIVE); len_b above
  * max_pages * page_size counts as that (FD_DEVERR_LEN_CLAMPED).

@@ -61,7 +61,13 @@ def _ex(plan, ws=P0, ws_bytes=None, out32=None, **kw):
 
 def test_attn_ex_refuses_plans_workspaces_and_alignment():
     plan = fd.fd_paged_plan_sms(1, 8, 2, 128, 16, 4, 0, 152, fd.FD_KV_E4M3)
-    assert plan.workspace_bytes > 0 and plan.blocks >= 1
+    up = lambda x: -(-x // 256) * 256
+    assert plan.blocks == 152 and plan.granule == 32
+    assert plan.workspace_bytes == up(2 * 152 * 4 * 128 * 4) + up(2 * 152 * 4 * 8) + up(152 * 16)
+    # a share is 64 KB of K and V at least
+    for HS, kv, want in ((64, fd.FD_KV_E4M3, 16), (128, fd.FD_KV_E4M3, 8), (128, fd.FD_KV_BF16, 4), (512, fd.FD_KV_BF16, 1)):
+        assert fd.fd_paged_plan_sms(1, 8, 2, HS, 16, 4, 0, 152, kv).min_share == want
+    assert _status(fd.fd_paged_plan_sms, 1, 8, 2, 128, 16, 4, 0, 1025, fd.FD_KV_BF16) == fd.FD_ERR_INVALID_ARG
     for name, value in (("B", 2), ("NH", 16), ("NKV", 4), ("HS", 64), ("page_size", 32), ("max_pages", 5), ("window", 7),
                         ("blocks", plan.blocks + 1), ("granule", 1), ("min_share", plan.min_share + 1), ("kv_dtype", 7),
                         ("num_sms", 0), ("workspace_bytes", 0)):

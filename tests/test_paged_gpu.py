@@ -231,6 +231,21 @@ def test_attn_nan_inside_the_band_reaches_only_its_group(kv):
     assert torch.isfinite(o32[0, 4:, :5]).all()
 
 
+def test_attn_rows_without_a_finite_score():
+    """Scores of -infinity have weight 0; a row of nothing else is zero, and beside a finite score they change nothing."""
+    P, HS = 16, 64
+    k, v = torch.zeros(3, 1, P, HS), torch.ones(3, 1, P, HS)
+    k[0, :, :, 0] = float("-inf")
+    k[1, :, 3:, 0] = float("-inf")
+    v[1, 0, :3] = torch.arange(3.0)[:, None]
+    k, v = k.bfloat16(), v.bfloat16()
+    q = torch.zeros(2, 1, HS).bfloat16()
+    q[:, :, 0] = 1
+    table = np.array([[0, -1], [0, 1]], dtype=np.int32)
+    _, o32, err = run_attn(BF16, q, k, None, v, None, table, [16, 32], 0)
+    assert err == 0 and (o32[0] == 0).all() and torch.allclose(o32[1], torch.ones(1, HS))
+
+
 @pytest.mark.parametrize("kv", [BF16, E4M3], ids=["bf16", "e4m3"])
 def test_attn_repairs_lengths_and_leaves_bad_pages_out(kv):
     P, N, HS = 16, 6, 64
