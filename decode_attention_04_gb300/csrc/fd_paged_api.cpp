@@ -264,7 +264,8 @@ int fd_paged_append(const void* k_new, const void* v_new, void* k_pages, void* v
                     float* v_scale, const int* table, const int* lens, const int* start, const int* count, int B,
                     int T, int NKV, int HS, int page_size, int num_pages, int max_pages, long long k_stride,
                     long long v_stride, int kv_dtype, fd_stream_t stream) {
-  const int rc = check_shape(B, NKV, NKV, HS, page_size, max_pages, kv_dtype);
+  // a batch of empty sequences has a table of no columns, and no token to write into it
+  const int rc = check_shape(B, NKV, NKV, HS, page_size, T == 0 && max_pages == 0 ? 1 : max_pages, kv_dtype);
   if (rc != FD_OK) return rc;
   if (T < 0 || num_pages <= 0 || (!start && T != B)) return FD_ERR_INVALID_ARG;
   const long long row = static_cast<long long>(NKV) * HS;

@@ -150,7 +150,8 @@ int fd_paged_attn_ex(const fd_paged_plan_t* plan, void* workspace, size_t worksp
  * A needed table entry that names no page raises FD_DEVERR_PAGE_ID and its
  * tokens are left out; so are tokens at positions from max_pages * page_size
  * on and rows outside [0, T). A token whose position would be negative (the one
- * of a sequence of length 0) is left out and raises nothing.
+ * of a sequence of length 0) is left out and raises nothing. With T == 0 nothing
+ * is done, and max_pages may be 0.
  * Errors: FD_ERR_INVALID_ARG, FD_ERR_UNSUPPORTED, FD_ERR_ALIGNMENT, FD_ERR_CUDA.
  */
 int fd_paged_append(const void* k_new, const void* v_new, void* k_pages, void* v_pages, float* k_scale,

@@ -109,6 +109,13 @@ def test_append_of_nothing_is_a_no_op():
     fd.fd_paged_append(*_append(B=0, T=0, start=None, table=None))
 
 
+def test_append_into_a_table_without_columns():
+    """Empty sequences that get nothing: their table has no columns and no address."""
+    fd.fd_paged_append(*_append(T=0, kn=None, vn=None, table=None, mp=0))
+    assert _status(fd.fd_paged_append, *_append(mp=0)) == fd.FD_ERR_INVALID_ARG
+    assert _status(fd.fd_paged_append, *_append(T=0, mp=-1)) == fd.FD_ERR_INVALID_ARG
+
+
 def test_bookkeeping_refuses():
     need = fd.fd_pages_workspace_bytes(2, 8)
     assert need == 4 * (8 + 4 * 2 + 256)
