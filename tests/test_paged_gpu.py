@@ -853,3 +853,44 @@ def test_attn_long_shares(kv, HS, NKV, G, P, lens):
             lim = (4 * HS * 2.0 ** -23 * mass + (2.0 ** -11 if kv == E4M3 else 2.0 ** -16) + 2.0 ** -20) * vv.abs().max()
             got = outs[0][b, h * G:(h + 1) * G].double()
             assert ((got - want).abs() <= lim + want.abs() * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("kv", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_pages_behind_four_billion_elements(kv):
+    """Append, attention and copy on pages at both ends of a pool of more than 2^32 elements: bit for bit what the same calls
+    give on a pool of a few pages. The pages between are never read."""
+    HS, NKV, P, G, lens, new = 512, 8, 128, 2, [300, 129], [130, 3]
+    far = 2 ** 32 // (NKV * P * HS) + 9
+    dt = torch.uint8 if kv == E4M3 else torch.bfloat16
+    small = np.array([[0, 1, 2], [3, 4, -1]], dtype=np.int32)
+    ids = np.array([far - 1, 2, far - 4, far - 2, 0])  # where the pages of the small pool lie in the large one
+    q = _values((2, NKV * G, HS), 1).bfloat16().to(DEV)
+    rows = _values((sum(new), 2, NKV, HS), 2).bfloat16().to(DEV)
+    old = [make_pool(kv, 5, NKV, P, HS, s)[:2] for s in (3, 4)]
+    results = []
+    fd.fd_get_device_error()
+    for N, at in ((6, np.arange(5)), (far, ids)):
+        where = torch.from_numpy(at).to(DEV)
+        spare = 5 if N == 6 else far - 3
+        pools, scales = [], []
+        for pages, scale in old:
+            pools.append(torch.empty((N, NKV, P, HS), dtype=dt, device=DEV))
+            pools[-1][where] = pages.to(DEV)
+            scales.append(None if scale is None else torch.zeros((N, NKV), device=DEV))
+            if scale is not None:
+                scales[-1][where] = scale.to(DEV)
+        table = d(np.where(small < 0, -1, at[np.maximum(small, 0)]).astype(np.int32))
+        ld = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        fd.fd_paged_append(rows, rows.data_ptr() + 2 * NKV * HS, *pools, *scales, table, ld, d(_starts(new)), None, 2, sum(new),
+                           NKV, HS, P, N, 3, 2 * NKV * HS, 2 * NKV * HS, kv)
+        out = torch.empty_like(q)
+        fd.fd_paged_attn(q, *pools, *scales, out, table, ld, 2, NKV * G, NKV, HS, P, N, 3, 0, 0.0, kv)
+        moves = torch.tensor([2, 0, int(at[0]), spare, int(at[4]), int(at[3])], dtype=torch.int32, device=DEV)
+        fd.fd_pages_copy(*pools, *scales, moves, 2, 1, N, NKV, P, HS, kv)
+        held = torch.cat([where, torch.tensor([spare], device=DEV)])
+        results.append([x[held].cpu() for x in pools + scales if x is not None] + [out.cpu()])
+        del pools
+    assert fd.fd_get_device_error() == 0
+    for x, y in zip(*results):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert torch.equal(results[1][0][5].view(torch.uint8), results[1][0][0].view(torch.uint8))
