@@ -33,9 +33,13 @@
 // E4M3 products are exact but for the other operand, which enters as a sum of
 // E4M3 terms, each in MMA columns of its own, term i scaled by 16^i so that it
 // has E4M3's full range: q = q0 + q1 / 16 (8 significant bits: all that bf16 has),
-// w = w0 + w1 / 16 + w2 / 256 (12 bits). The columns are added in fp32 at the end. 48 columns
+// w = w0 + w1 / 16 + ... + w5 / 16^5 (24 bits, as many as the sum has, and nothing is dropped above 2^-30: with three
+// terms weights below 2^-18 were, which in a long band are the output where the largest weight's value is
+// small). The columns are added in fp32 at the end. 96 columns
 // instead of 16 cost the tensor cores nothing here: an MMA takes as long as reading its
-// 128-row operand. bf16 takes q as it is and w = w0 + w1 (16 bits).
+// 128-row operand. Head dim 512 with 16 rows has tensor memory for 48 columns: the terms go there in pairs, both
+// unscaled in one column, by two MMAs one behind the other, pairs 256 apart (nothing is dropped above 2^-26).
+// bf16 takes q as it is and w = w0 + w1 (16 bits).
 //
 // Scales. K's multiplies the score. V's enters the weight, w_p = 2^(t_p - m),
 // t_p = s_p log2(e) + log2(vs): m follows the largest t, so that w fits E4M3 whatever
@@ -168,6 +172,13 @@ template <int SW>
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo) {
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
          (static_cast<uint64_t>((8 * SW) >> 4) << 32) | (1ull << 46) | (static_cast<uint64_t>(SW == 128 ? 2 : 4) << 61);
+}
+
+// The same without a swizzle, MN-major: 16 bytes of a row, rows 16 bytes apart; LBO is the distance between 8-row groups
+// along K, SBO between column blocks of 16 bytes.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((8 * 16) >> 4) << 16) |
+         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46);
 }
 
 // Byte offset of 16-byte piece `piece` of row `row` in rows of SW bytes.
@@ -355,13 +366,14 @@ struct Cfg {
   static constexpr int SLOT = CH * CHUNK;
   static constexpr int KSTEP = 32 / EB;                // K of one MMA (32 bytes)
   static constexpr int QT = KV8 ? 2 : 1;               // terms of q
-  static constexpr int PT = KV8 ? 3 : 2;               // terms of a weight
+  static constexpr int PT = KV8 ? 6 : 2;               // terms of a weight
+  static constexpr int PP = KV8 && HS * NQ > 4096 ? 2 : 1;  // terms that share a column
   static constexpr int NS = round16(QT * NQ);          // columns of S
-  static constexpr int NP = round16(PT * NQ);          // columns of O
+  static constexpr int NP = round16(PT / PP * NQ);     // columns of O
   static constexpr int COLS = pow2_cols(2 * NS + 2 * NB * NP);
   static constexpr int O_COL = 2 * NS;
   static constexpr int Q_BYTES = NB * CH * NS * SW;
-  static constexpr int P_BYTES = NP * kTile * EB;
+  static constexpr int P_BYTES = PP * NP * kTile * EB;
   static constexpr int RED_BYTES = (2 * 11 + 4) * NQ * 4;
   static constexpr int Q_STRIDE = (Q_BYTES + 1023) / 1024 * 1024;
   static constexpr int RING_ROOM = 227 * 1024 - 2 * Q_STRIDE - 2 * P_BYTES - RED_BYTES - kLenCache * 4 - 2048;
@@ -379,15 +391,16 @@ struct Cfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tensor memory address; share; edge[2]
   static constexpr int SMEM = OFF_MISC + 64 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(P_BYTES % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms are aligned");
+  static_assert(2 * NS + 2 * NB * NP <= 512, "tensor memory");
+  static_assert(Q_STRIDE % 1024 == 0, "swizzle atoms are aligned");
   static_assert(OFF_BAR % 8 == 0, "barriers");
   static constexpr int RK = RING / 2, RV = RING - RK;  // K's slots, then V's
   static_assert(RK >= 2, "two slots of each of K and V");
   // Instruction descriptor: D f32; A and B E4M3 (0) or bf16 (1 in bits 7 and
-  // 10); bit 15: A is MN-major; N / 8 at 17, M / 16 at 24.
+  // 10); bits 15 and 16: A and B are MN-major; N / 8 at 17, M / 16 at 24.
   static constexpr uint32_t IDESC_QK = (1u << 4) | (KV8 ? 0u : (1u << 7) | (1u << 10)) |
                                        (static_cast<uint32_t>(NS >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
-  static constexpr uint32_t IDESC_PV = (1u << 4) | (KV8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 15) |
+  static constexpr uint32_t IDESC_PV = (1u << 4) | (KV8 ? 0u : (1u << 7) | (1u << 10)) | (3u << 15) |
                                        (static_cast<uint32_t>(NP >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 };
 
@@ -428,14 +441,41 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t c) {
   return __half22float2(__half2(h));
 }
 
-// x = c0 + c1 / 16 + c2 / 256 + ...: the next E4M3 term of a pair; x becomes
-// what is left, times 16. x is at most 448 in size.
-__device__ __forceinline__ uint16_t next_term(float2& x) {
+// x = c0 + c1 / 16 + c2 / 256 + ... (by = 16): the next E4M3 term of a pair; x becomes
+// what is left, times `by`. x is at most 448 in size.
+__device__ __forceinline__ uint16_t next_term(float2& x, float by) {
   const uint16_t c = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
   const float2 y = e4m3x2_to_f32(c);
-  x.x = (x.x - y.x) * 16.f;
-  x.y = (x.y - y.y) * 16.f;
+  x.x = (x.x - y.x) * by;
+  x.y = (x.y - y.y) * by;
   return c;
+}
+
+// The same of a pair of fp16 values, exactly: what a term leaves is a multiple of x's last place.
+__device__ __forceinline__ uint16_t next_term(__half2& x, float by) {
+  const uint16_t c = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+  x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+  if (by != 1.f) x = __hmul2(x, __float2half2_rn(by));
+  return c;
+}
+
+// Six terms of a pair of weights of at most 2^8, PP of them to a column (the columns 16^PP apart). In fp16 where that
+// holds what is left (its first 11 bits, after four terms the rest): half as many instructions as in fp32.
+template <int PP>
+__device__ __forceinline__ void six_terms(float2 w, uint16_t (&c)[6]) {
+  constexpr float kLast = PP == 1 ? 16.f : 256.f, kFirst = PP == 1 ? 16.f : 1.f;  // behind the terms that end a column, the others
+  __half2 x = __floats2half2_rn(w.x, w.y);
+  const float2 hi = __half22float2(x);
+  c[0] = next_term(x, kFirst);
+  c[1] = next_term(x, kLast);
+  c[2] = next_term(x, kFirst);
+  const float2 left = __half22float2(x);
+  constexpr float kScale = PP == 1 ? 4096.f : 256.f;  // of what is left by now
+  float2 z = make_float2(fmaf(w.x - hi.x, kScale, left.x), fmaf(w.y - hi.y, kScale, left.y));
+  c[3] = next_term(z, kLast);
+  x = __floats2half2_rn(z.x, z.y);
+  c[4] = next_term(x, kFirst);
+  c[5] = next_term(x, kLast);
 }
 
 struct Maps {
@@ -699,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
               }
   #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const uint32_t term = next_term(y);
+                const uint32_t term = next_term(y, 16.f);
                 if (i & 1) w[j][i / 2] |= term << 16;
                 else w[j][i / 2] = term;
               }
@@ -823,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       // ------------------------------------------------------------ values: O^T += V^T P^T
       const bool issuer = elect_one();
       const uint64_t v_desc = smem_desc<C::SW>(base, C::CH > 1 ? C::CHUNK : C::SLOT);
-      const uint64_t p_desc = smem_desc<128>(base + C::OFF_P, 16);
+      const uint64_t p_desc = smem_desc_plain(base + C::OFF_P, 16 * kTile);
       int slot = C::RK;
       uint32_t turn = 0;
       // bit g, of group g: parity of v_clean's phase, of o_free's, and whether O was used
@@ -855,18 +895,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           if (issuer) {
             const uint32_t d = tmem + C::O_COL + C::NP * (g * C::NB + p);
             const uint64_t vd = v_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
-              auto step = [&](int kk) {
-              umma<C::KV8>(d, vd + ((kk * C::KSTEP * C::SW) >> 4),
-                           pd + ((kk * 32 / 128 * (C::NP * 128) + kk * 32 % 128) >> 4), C::IDESC_PV, kk > 0 ? 1u : keep);
-            };
-            constexpr int kSteps = kTile / C::KSTEP;
-            if (nk == kSteps) {
-#pragma unroll
-              for (int kk = 0; kk < kSteps; ++kk) step(kk);
-            } else {
+            // in loops: the block's code has to fit the instruction cache (unrolled: ragged batch E4M3 104 us, so 98)
 #pragma unroll 1
-              for (int kk = 0; kk < nk; ++kk) step(kk);
-            }
+            for (int t = 0; t < C::PP; ++t)
+#pragma unroll 1
+              for (int kk = 0; kk < nk; ++kk)
+                umma<C::KV8>(d, vd + ((kk * C::KSTEP * C::SW) >> 4),
+                             pd + ((t * C::NP * kTile * C::EB + kk * C::KSTEP * 16) >> 4), C::IDESC_PV,
+                             (t | kk) != 0 ? 1u : keep);
             umma_commit(empty + 8 * slot);
             if (p == C::NB - 1) umma_commit(pv_done + 8 * g);
           }
@@ -953,8 +989,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     float2 ksvs = scales(cur, page);
     named_bar_sync(BAR_BOTH, 2 * kSoft);
     if (grp == 0 && tq == 0) mbar_arrive(q_ready);
-    next_tile(a, lens, walk);
-    next_tile(a, lens, walk);
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) next_tile(a, lens, walk);
     Tile nxt = walk.t;
     int next_page = entry(nxt);
     // Per row: the reference (the running maximum less the bias), this thread's share of the sum. A lane
@@ -965,8 +1001,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     float ref_lane = kNone;
     int i = grp, seg_seen = -1, cleared = 0;
     while (cur.ok) {
-      next_tile(a, lens, walk);
-      next_tile(a, lens, walk);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) next_tile(a, lens, walk);
       const Tile after = walk.t;
       const int after_page = entry(after);
       const float2 next_ksvs = scales(nxt, next_page);
@@ -1064,32 +1100,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       // P(i) -> the group's buffer; its last reader, P.V(i - 2), must be done
       if (u >= 1) warp_wait(pv_done + 8 * grp, (u - 1) & 1, failed);
       if (tq == 0) edge[grp] = clear;
-      unsigned char* pbuf = smem + C::OFF_P + grp * C::P_BYTES;
+      // Column n of a position: byte or bf16 n % 16 or n % 8 of its 16 bytes in a block of columns. So a position's
+      // columns leave its thread by a few 16-byte stores (a byte each: 96 stores for 16 rows).
+      constexpr int kBlocks = C::PP * C::NP * C::EB / 16;
+      uint32_t col[4 * kBlocks] = {};
       if constexpr (C::KV8) {
-        // byte pl of row n: 16-byte piece pl / 16, swizzled by n % 8
-        unsigned char* at = pbuf + (pl & 15);
 #pragma unroll
-        for (int r = 0; r < C::NQ; r += 2) {
-          float2 x = make_float2(w[r], w[r + 1]);
+        for (int r = 0; r < C::NQ; r += 4) {
+          uint16_t lo[C::PT], hi[C::PT];
+          six_terms<C::PP>(make_float2(w[r], w[r + 1]), lo);
+          six_terms<C::PP>(make_float2(w[r + 2], w[r + 3]), hi);
 #pragma unroll
-          for (int j = 0; j < 3; ++j) {
-            const uint16_t code = next_term(x);
-            const int n = j * C::NQ + r;
-            at[n * 128 + (((pl >> 4) ^ (n & 7)) << 4)] = static_cast<unsigned char>(code & 0xff);
-            at[(n + 1) * 128 + (((pl >> 4) ^ ((n + 1) & 7)) << 4)] = static_cast<unsigned char>(code >> 8);
-          }
+          for (int j = 0; j < C::PT; ++j)
+            col[(j % C::PP * C::NP + j / C::PP * C::NQ + r) / 4] = lo[j] | (static_cast<uint32_t>(hi[j]) << 16);
         }
       } else {
-        unsigned char* half = pbuf + (pl >> 6) * C::NP * 128;
-        const int piece = (pl & 63) >> 3, in = (pl & 7) * 2;
 #pragma unroll
-        for (int r = 0; r < C::NQ; ++r) {
-          const uint16_t hi = f32_to_bf16_bits(w[r]);
-          const uint16_t lo16 = f32_to_bf16_bits(w[r] - bf16_bits_to_f32(hi));
-          *reinterpret_cast<uint16_t*>(half + swizzled<128>(r, piece) + in) = hi;
-          *reinterpret_cast<uint16_t*>(half + swizzled<128>(C::NQ + r, piece) + in) = lo16;
+        for (int r = 0; r < C::NQ; r += 2) {
+          float x = w[r], y = w[r + 1];
+#pragma unroll
+          for (int j = 0; j < C::PT; ++j) {
+            const uint16_t lo = f32_to_bf16_bits(x), hi = f32_to_bf16_bits(y);
+            col[(j * C::NQ + r) / 2] = lo | (static_cast<uint32_t>(hi) << 16);
+            x -= bf16_bits_to_f32(lo);
+            y -= bf16_bits_to_f32(hi);
+          }
         }
       }
+      uint4* pbuf = reinterpret_cast<uint4*>(smem + C::OFF_P + grp * C::P_BYTES) + pl;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+        pbuf[b * kTile] = make_uint4(col[4 * b], col[4 * b + 1], col[4 * b + 2], col[4 * b + 3]);
       fence_proxy_async_smem();  // P -> the tensor cores' view of shared memory
       tc_fence_before();
       mbar_arrive(p_ready + 8 * grp);
@@ -1166,8 +1207,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 #pragma unroll
             for (int j = 0; j < kTerms; ++j) {
               const int term = part_no * kTerms + j;
-              if (term >= C::PT) break;  // columns of no term hold anything
-              const float by = !C::KV8 || term == 0 ? 1.f : term == 1 ? 0.0625f : 0.00390625f;
+              if (term >= C::PT / C::PP) break;  // columns of no term hold anything
+              const float by = C::KV8 ? __uint_as_float(static_cast<uint32_t>(127 - 4 * C::PP * term) << 23) : 1.f;
 #pragma unroll
               for (int r = 0; r < C::NQ; ++r) x[r] += fac[k * C::NQ + r] * by * o[j * C::NQ + r];
             }

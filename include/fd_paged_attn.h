@@ -102,8 +102,10 @@ int fd_paged_plan_sms(int B, int NH, int NKV, int HS, int page_size, int max_pag
  * max_pages * page_size counts as that (FD_DEVERR_LEN_CLAMPED).
  * Arithmetic, E4M3: q is split into two E4M3 terms (exact for elements within
  * 2^13 of the row's largest, else off by 2^-21 of that) and the softmax
- * weights, times their block's V scale, into three (off by 2^-12 of themselves
- * or 2^-21 of the largest); products accumulate in fp32. bf16: q enters as it
+ * weights, times their block's V scale, into six (off by 2^-24 of themselves or
+ * 2^-32 of the largest; HS 512 with NH / NKV > 8: 2^-30 of the largest, so n
+ * positions of weights that are that small may add n times as much to the
+ * error); products accumulate in fp32. bf16: q enters as it
  * is, the weights as two bf16 terms (2^-16).
  * fd_paged_attn makes its plan for the current device and uses a workspace
  * the library owns, one per (device, stream): the first call for a pair
