@@ -41,9 +41,10 @@
 // unscaled in one column, by two MMAs one behind the other, pairs 256 apart (nothing is dropped above 2^-26).
 // bf16 takes q as it is and w = w0 + w1 (16 bits).
 //
-// Scales. K's multiplies the score. V's enters the weight, w_p = 2^(t_p - m),
-// t_p = s_p log2(e) + log2(vs): m follows the largest t, so that w fits E4M3 whatever
-// the scales are, and the row's sum l = sum 2^(s_p log2(e) - m) has the same reference.
+// Scales. K's multiplies the score. V's multiplies the weight, in units of 2^vref, vref the exponent of the
+// largest V scale that the group has met in the segment: w_p = 2^(s_p log2(e) - m) * (vs / 2^vref), so that w fits
+// E4M3 whatever the scales are, and the output is multiplied by 2^vref at the end. The maximum m and the row's sum
+// l = sum 2^(s_p log2(e) - m) do not know V's scales: a block whose scale is 0 counts in l as any other does.
 
 #include <cuda.h>  // CUtensorMap (descriptor type only; the encoder comes from the runtime)
 #include <cudaTypedefs.h>
@@ -374,13 +375,13 @@ struct Cfg {
   static constexpr int O_COL = 2 * NS;
   static constexpr int Q_BYTES = NB * CH * NS * SW;
   static constexpr int P_BYTES = PP * NP * kTile * EB;
-  static constexpr int RED_BYTES = (2 * 11 + 4) * NQ * 4;
+  static constexpr int RED_BYTES = (2 * 11 + 4) * NQ * 4 + 64;
   static constexpr int Q_STRIDE = (Q_BYTES + 1023) / 1024 * 1024;
   static constexpr int RING_ROOM = 227 * 1024 - 2 * Q_STRIDE - 2 * P_BYTES - RED_BYTES - kLenCache * 4 - 2048;
   static constexpr int RING = RING_ROOM / SLOT < 24 ? RING_ROOM / SLOT : 24;  // slots: all the shared memory there is
   static constexpr int OFF_Q = RING * SLOT;
   static constexpr int OFF_P = OFF_Q + 2 * Q_STRIDE;
-  // f32, of each group 11 NQ, of both 4 NQ: the groups' statistics
+  // f32, of each group 11 NQ, of both 4 NQ: the groups' statistics; int: exponents of V's scales
   static constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
   static constexpr int OFF_QMUL = OFF_RED + RED_BYTES;  // f32 [kQRing][16]
   static constexpr int OFF_LEN = OFF_QMUL + kQRing * 16 * 4;
@@ -482,15 +483,29 @@ struct Maps {
   CUtensorMap k, v;
 };
 
+// 2^n for n <= 127 (0 below 2^-126).
+__device__ __forceinline__ float pow2_of(int n) {
+  return n < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
+}
+
+// The exponent of a scale, of zero kNoScale.
+constexpr int kNoScale = -150;
+__device__ __forceinline__ int exponent_of(float s) {
+  const uint32_t u = __float_as_uint(s) & 0x7fffffffu;
+  return u >= 0x00800000u ? static_cast<int>(u >> 23) - 127 : 31 - __clz(u) - 149;
+}
+
 // Which units a block's share breaks: written for the merge.
 struct Cut {
   int b, kvh;
   int c0, c1;  // the unit lies in the shares c0 .. c1; c0 < 0: the share ends where a unit does
 };
 
-// The smallest power of the running reference that is moved: weights are at
-// most 2^kLazy times the bias, which keeps them within E4M3's 448.
-constexpr float kLazy8 = 4.f, kBias8 = 4.f;
+// The smallest power of the running reference that is moved: 2^(s - m) is at most 2^(kLazy + kBias). E4M3: that is
+// 2^7, and V's scale in units of 2^vref is below 2, which keeps weights within E4M3's 448. A higher bias leaves
+// smaller weights above what the terms drop, a lower one moves the reference less often: terms with a column each drop
+// less and take the lower one (3 / 4 / 5 before a move: ragged batch E4M3 107 / 106 / 105 us, 4 x 131072 MQA 97.7 / 97.6 / 97.6).
+constexpr float kTop8 = 7.f, kLazy8 = 5.f, kLazy8Shared = 3.f;
 constexpr float kLazy16 = 8.f, kBias16 = 0.f;
 
 template <class C>
@@ -949,7 +964,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   } else {
     // ---------------------------------------------- softmax / epilogue warps
     regs_inc<kRegsSoft>();
-    constexpr float kLazy = C::KV8 ? kLazy8 : kLazy16, kBias = C::KV8 ? kBias8 : kBias16;
+    constexpr float kLazy = !C::KV8 ? kLazy16 : C::PP == 1 ? kLazy8 : kLazy8Shared;
+    constexpr float kBias = !C::KV8 ? kBias16 : kTop8 - kLazy;
     const int grp = (warp - W_SOFT0) / kSoftWarps;  // takes the tiles i with i % 2 == grp
     const int sw = (warp - W_SOFT0) % kSoftWarps;
     const int quarter = warp & 3;   // the TMEM lane quarter this warp may access
@@ -977,6 +993,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     float* refs = sums + 4 * C::NQ;
     float* fac = refs + C::NQ;
     float2* stat = reinterpret_cast<float2*>(red + 2 * 11 * C::NQ);
+    // exponents of V's scales: the largest of each warp's positions in a tile; of each group's in a segment, and the
+    // part of it that the output takes
+    int* vtops = reinterpret_cast<int*>(red + 26 * C::NQ) + 4 * grp;
+    int* vrefs = reinterpret_cast<int*>(red + 26 * C::NQ) + 8;
     const uint32_t o_cols = tmem + tlane + C::O_COL;
 
     // This group's tiles: the current one and the next. The look-ups are in
@@ -999,6 +1019,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     constexpr int kPer = 32 / C::NQ; // lanes that end with the same row
     float ref[C::NQ], l_part[C::NQ];
     float ref_lane = kNone;
+    // V's scales: the exponent vref that they are held in units of, 2^-vref as two factors (alone it may not be a
+    // float), and the least scale that moves it.
+    int vref;
+    float vunit[2], vlim;
+    auto set_vref = [&](int e) {
+      vref = e;
+      vunit[0] = pow2_of(-(e >> 1));
+      vunit[1] = pow2_of((e >> 1) - e);
+      vlim = e == kNoScale ? __uint_as_float(1) : e < 127 ? pow2_of(e + 1) : -kNegInf;
+    };
+    set_vref(kNoScale);
     int i = grp, seg_seen = -1, cleared = 0;
     while (cur.ok) {
 #pragma unroll 1
@@ -1010,6 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       if (cur.seg != seg_seen) {
         seg_seen = cur.seg;
         ref_lane = kNone;
+        set_vref(kNoScale);
 #pragma unroll
         for (int r = 0; r < C::NQ; ++r) {
           ref[r] = kNone;
@@ -1028,33 +1060,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_arrive(s_free + 8 * grp);
 
       // the segment's multipliers were in place before its score MMAs were issued
-      // sc: log2 of the weight for the row's sum; t: for the product with V's codes
-      float sc[C::NQ], t[C::NQ];
+      float sc[C::NQ];  // log2 of the weight
       if constexpr (C::KV8) {
-        // a scale of 0 counts as 2^-150: its weights vanish beside any other's
-        const float lvs = ksvs.y == 0.f ? -150.f : log2f(ksvs.y);
         const float4* qm = reinterpret_cast<const float4*>(qmul + (cur.seg & (kQRing - 1)) * 16);
 #pragma unroll
         for (int r = 0; r < C::NQ; r += 4) {
           const float4 m = qm[r / 4];
           const float mul[4] = {ksvs.x * m.x, ksvs.x * m.y, ksvs.x * m.z, ksvs.x * m.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 4; ++j)
             sc[r + j] = live ? (s[r + j] + s[C::NQ + r + j] * 0.0625f) * mul[j] : kNegInf;
-            t[r + j] = sc[r + j] + lvs;
-          }
         }
       } else {
 #pragma unroll
-        for (int r = 0; r < C::NQ; ++r) t[r] = sc[r] = live ? s[r] * a.scale_log2 : kNegInf;
+        for (int r = 0; r < C::NQ; ++r) sc[r] = live ? s[r] * a.scale_log2 : kNegInf;
       }
       // The tile's row maxima. Most tiles move no reference and have every row live: one
       // barrier tells the group so.
-      const float wmax = rowreduce<C::NQ>(t, lane, MaxOp());
+      const float wmax = rowreduce<C::NQ>(sc, lane, MaxOp());
       bool clear = false;
-      if (named_bar_or(BAR_GROUP + grp, kSoft, dead_row || wmax > ref_lane + (kLazy + kBias))) {
+      if (named_bar_or(BAR_GROUP + grp, kSoft,
+                       dead_row || wmax > ref_lane + (kLazy + kBias) || (C::KV8 && ksvs.y >= vlim))) {
         if (dead_row && cur.pos + pl >= cur.lo && cur.pos + pl < cur.end) atomicOr(&g_device_error, FD_DEVERR_PAGE_ID);
         if (lane % kPer == 0) part[(lane / kPer) * kSoftWarps + sw] = wmax;
+        if constexpr (C::KV8) {
+          const int vtop = __reduce_max_sync(0xffffffffu, exponent_of(ksvs.y));
+          if (lane == 0) vtops[sw] = vtop;
+        }
         clear = named_bar_or(BAR_GROUP + grp, kSoft, dead_row);
         auto row_max = [&](int r) {
           const float4 t4 = *reinterpret_cast<const float4*>(part + r * kSoftWarps);
@@ -1064,7 +1096,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const float ml = row_max(lane / kPer);
         if (ml > ref_lane + (kLazy + kBias)) ref_lane = ml - kBias;  // false for -inf and NaN
         float alpha[C::NQ];
+        float valpha = 1.f;  // of the accumulators beside alpha
         bool resc = false;
+        if constexpr (C::KV8) {
+          const int4 v4 = *reinterpret_cast<const int4*>(vtops);
+          const int to = max(max(vref, max(v4.x, v4.y)), max(v4.z, v4.w));
+          valpha = pow2_of(vref - to);
+          resc = to != vref;
+          set_vref(to);
+        }
 #pragma unroll
         for (int r = 0; r < C::NQ; ++r) {
           const float mt = row_max(r);
@@ -1084,17 +1124,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             float o[16];
             tmem_load<16>(o_cols + C::NP * C::NB * grp + x, o);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] *= alpha[r % C::NQ];
+            for (int r = 0; r < 16; ++r) o[r] *= alpha[r % C::NQ] * valpha;
             tmem_st16(o_cols + C::NP * C::NB * grp + x, o);
           }
           tmem_st_wait();
         }
       }
+      const float vs = C::KV8 ? ksvs.y * vunit[0] * vunit[1] : 1.f;
       float w[C::NQ];
 #pragma unroll
       for (int r = 0; r < C::NQ; ++r) {
-        w[r] = exp2f(t[r] - ref[r]);
-        l_part[r] += C::KV8 ? exp2f(sc[r] - ref[r]) : w[r];
+        w[r] = exp2f(sc[r] - ref[r]);
+        l_part[r] += w[r];
+        if constexpr (C::KV8) w[r] *= vs;
       }
 
       // P(i) -> the group's buffer; its last reader, P.V(i - 2), must be done
@@ -1172,6 +1214,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         if (tq < C::NQ) {
           const float4 t4 = *reinterpret_cast<const float4*>(sums + tq * kSoftWarps);
           stat[grp * C::NQ + tq] = make_float2(refs[tq], (t4.x + t4.y) + (t4.z + t4.w));  // fixed order
+          if (tq == 0) vrefs[grp] = vref;
         }
         if (both) named_bar_sync(BAR_BOTH, 2 * kSoft);
         if (tq < C::NQ) {
@@ -1181,14 +1224,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           const float m = fmaxf(s0.x, s1.x);
           const float e0 = exp2f(s0.x - m), e1 = exp2f(s1.x - m);
           const float l = e0 * s0.y + e1 * s1.y;
-          const float by = direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-          fac[tq] = e0 * by;
-          fac[C::NQ + tq] = e1 * by;
+          const float by = l == 0.f ? 0.f : 1.f / l;
+          if constexpr (C::KV8) {  // times 2^vref, but for 2^-64 that the output takes where that is very small
+            const int v_other = both ? vrefs[1 - grp] : vref, low = max(vref, v_other) < -64 ? -64 : 0;
+            fac[tq] = e0 * by * pow2_of((grp == 0 ? vref : v_other) - low);
+            fac[C::NQ + tq] = e1 * by * pow2_of((grp == 1 ? vref : v_other) - low);
+            if (tq == 0) vrefs[2 + grp] = low;
+          } else {
+            fac[tq] = e0 * by;
+            fac[C::NQ + tq] = e1 * by;
+          }
           if (!direct && tq < G && (!both || grp == 0))
             reinterpret_cast<float2*>(a.ws_ml)[static_cast<size_t>(slot) * G + tq] = make_float2(m, l);
         }
         named_bar_sync(BAR_GROUP + grp, kSoft);
         tc_fence_after();
+        const bool low = C::KV8 && vrefs[2 + grp] != 0;
         // with one block of dims the groups share its rows
         const int row0 = both && C::NB == 1 ? grp * (C::NQ / 2) : 0;
         const int row1 = min(G, both && C::NB == 1 ? row0 + C::NQ / 2 : C::NQ);
@@ -1210,8 +1261,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
               if (term >= C::PT / C::PP) break;  // columns of no term hold anything
               const float by = C::KV8 ? __uint_as_float(static_cast<uint32_t>(127 - 4 * C::PP * term) << 23) : 1.f;
 #pragma unroll
-              for (int r = 0; r < C::NQ; ++r) x[r] += fac[k * C::NQ + r] * by * o[j * C::NQ + r];
+              for (int r = 0; r < C::NQ; ++r) x[r] += fac[k * C::NQ + r] * (by * o[j * C::NQ + r]);
             }
+          }
+          if (low) {
+#pragma unroll
+            for (int r = 0; r < C::NQ; ++r) x[r] *= 0x1p-64f;
           }
           const int d = mb * 128 + pl;  // O^T lanes are head dims
           if (pl < C::DB) {
@@ -1272,7 +1327,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 
 constexpr int kMergeThreads = 256;
 
-// A unit that lies in the shares c0 .. c1 left a partial in each. Block c in
+// A unit that lies in the shares c0 .. c1 left a partial in each: the mean of its values, as the output has them (in
+// range whatever V's scales are), the reference and the sum of its weights. Block c in
 // [c0, c1) takes its part of the unit's G * HS outputs: one item is four dims
 // of a row, whose partials are summed by several threads and then in fixed
 // order.
@@ -1326,9 +1382,9 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
         for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
         float l = 0.f;
         auto one = [&](int p, const float2& v) {
-          const float f = exp2f(v.x - m);
+          const float f = exp2f(v.x - m) * v.y;
           factor[(q - r0) * parts + p] = f;
-          l += f * v.y;
+          l += f;
         };
 #pragma unroll
         for (int j = 0; j < kHeld; ++j)

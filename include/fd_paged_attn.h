@@ -60,7 +60,7 @@ enum {
  * `min_share` pieces more than it has, and dealt to
  * `blocks` thread blocks in equal consecutive shares on the device (the
  * lengths are read there): a block may end one band and begin the next. A band
- * that lies in several shares leaves one (O, m, l) partial in each, which a
+ * that lies in several shares leaves one partial in each, which a
  * second kernel merges.
  */
 typedef struct {
@@ -103,9 +103,10 @@ int fd_paged_plan_sms(int B, int NH, int NKV, int HS, int page_size, int max_pag
  * Arithmetic, E4M3: q is split into two E4M3 terms (exact for elements within
  * 2^13 of the row's largest, else off by 2^-21 of that) and the softmax
  * weights, times their block's V scale, into six (off by 2^-24 of themselves or
- * 2^-32 of the largest; HS 512 with NH / NKV > 8: 2^-30 of the largest, so n
- * positions of weights that are that small may add n times as much to the
- * error); products accumulate in fp32. bf16: q enters as it
+ * 2^-32 of the largest weight times the largest scale; HS 512 with NH / NKV > 8:
+ * 2^-30 of that, so n positions of weights that are that small may add n times
+ * as much to the error); products accumulate in fp32. Every scale that is not
+ * negative is taken, 0 and subnormals too. bf16: q enters as it
  * is, the weights as two bf16 terms (2^-16).
  * fd_paged_attn makes its plan for the current device and uses a workspace
  * the library owns, one per (device, stream): the first call for a pair

@@ -8,7 +8,7 @@ import torch
 
 import decode_attention_04_gb300 as fd
 import paged_ref as ref
-from test_paged_gpu import BF16, E4M3, d
+from test_paged_gpu import BF16, E4M3, _values, d, make_pool, make_table, run_attn
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -69,3 +69,124 @@ def test_small_weights_behind_a_large_one(kv, HS, G, bits, n, sink, B):
     err = (out32.double().cpu() - want).abs()
     assert (err <= lim).all(), f"{(err / lim).max():.2f} of the bound, {(err / want).max():.2e} of the output"
     assert ((out.double().cpu() - want).abs() <= lim + want * 2.0 ** -8).all()
+
+
+def check(kv, q, k, ks, v, vs, table, lens, out16, out32, e2):
+    """Against the 64-bit reference; e2 bounds what the weights and the sums lose, relative to the largest value of the row.
+    Outputs below 2^-126 are multiples of fp32's least value: its half, 2^-150, is added, and bf16's, 2^-134."""
+    HS = q.shape[2]
+    kr, vr = (k.double().numpy(), v.double().numpy()) if kv == BF16 else (k.numpy(), v.numpy())
+    want, big, mass = ref.attend(q.double().numpy(), kr, vr, None if ks is None else ks.numpy(),
+                                 None if vs is None else vs.numpy(), table, lens, 0, HS ** -0.5, k.shape[0])
+    lim = ((4 * HS * 2.0 ** -23 * mass + e2 + 2.0 ** -20) * big)[..., None] + 2.0 ** -150
+    got = out32.double().numpy()
+    assert np.isfinite(got).all(), f"{(~np.isfinite(got)).sum()} of {got.size} are not finite"
+    err = np.abs(got - want)
+    assert (err <= lim).all(), f"{(err / lim).max():.2f} of the bound"
+    assert (np.abs(out16.double().numpy() - want) <= lim + np.abs(want) * 2.0 ** -8 + 2.0 ** -134).all()
+    return want
+
+
+def lost(n):
+    """For n positions: weights are off by 2^-24 of themselves or 2^-30 of the largest weight times the largest scale, which
+    counts 2^5 times where the largest code under that scale is 448 / 2^5 (the pools here have larger ones); sums of n
+    products, 32 an addition, by 2^-23 an addition."""
+    return 2.0 ** -24 + n * 2.0 ** -25 + (n / 32 + 64) * 2.0 ** -23
+
+
+def spans(n, P):
+    """Runs of positions that are zeroed, by what they are to the kernel: its tiles are 128 positions long, taken by two
+    groups in turn, and a share begins at any multiple of 32."""
+    yield "first tile", (0, 128)
+    yield "second tile", (128, 256)
+    yield "third tile", (256, 384)
+    yield "first two", (0, 256)
+    yield "last page", ((n - 1) // P * P, n)
+    yield "all but the last page", (0, (n - 1) // P * P)
+    yield "a piece", (n // 2 // P * P, n // 2 // P * P + max(P, 32))
+    yield "all", (0, n)
+
+
+@pytest.mark.parametrize("codes", ["zero codes", "codes"])
+@pytest.mark.parametrize("level", [-6, 0, 20, -120])
+@pytest.mark.parametrize("HS,G,P", [(64, 1, 16), (128, 4, 16), (128, 8, 32), (256, 9, 16), (512, 16, 128), (512, 3, 16)])
+def test_blocks_of_v_scale_zero(HS, G, P, level, codes):
+    """Blocks whose V scale is zero - what the writer makes of zeros - count in the softmax's sum and add nothing: in any tile
+    of a band that lies in one share or in several, beside scales of 2^level."""
+    for n in (129, 200, 400, 257 * P // 16 + 2300):
+        for what, (lo, hi) in spans(n, P):
+            N = -(-n // P) + 1
+            k, ks, _ = make_pool(E4M3, N, 2, P, HS, n)
+            v, vs, _ = make_pool(E4M3, N, 2, P, HS, n + 1)
+            table = make_table([n], P, N, N, n)
+            vs = torch.exp2(torch.randint(level, level + 2, vs.shape, generator=torch.Generator().manual_seed(n)).float())
+            pages = table[0][lo // P:-(-min(hi, n) // P)]
+            vs[pages, 0] = 0.0
+            if codes == "zero codes":
+                v[pages, 0] = 0
+            q = _values((1, 2 * G, HS), 7).bfloat16()
+            out16, out32, err = run_attn(E4M3, q, k, ks, v, vs, table, [n], 0)
+            assert err == 0
+            want = check(E4M3, q, k, ks, v, vs, table, [n], out16, out32, lost(n))
+            if what == "all":
+                assert (want[0, :G] == 0).all() and (out32[0, :G] == 0).all()
+
+
+@pytest.mark.parametrize("tiny", [0.0, 2.0 ** -149, 2.0 ** -126, 2.0 ** -124, 2.0 ** -60])
+@pytest.mark.parametrize("HS,G,P", [(128, 4, 16), (512, 16, 128)])
+def test_one_token_of_a_tiny_v_scale(HS, G, P, tiny):
+    """A last token alone in its page and its tile; and the same scale in every block."""
+    n = 2 * P + 1 if P == 128 else 129
+    N = -(-n // P)
+    k, ks, _ = make_pool(E4M3, N, 1, P, HS, 3)
+    v, vs, _ = make_pool(E4M3, N, 1, P, HS, 4)
+    table = make_table([n], P, N, N, 5)
+    q = _values((1, G, HS), 7).bfloat16()
+    vs[table[0, -1], 0] = tiny
+    out16, out32, err = run_attn(E4M3, q, k, ks, v, vs, table, [n], 0)
+    assert err == 0
+    check(E4M3, q, k, ks, v, vs, table, [n], out16, out32, lost(n))
+    vs[:] = tiny
+    out16, out32, err = run_attn(E4M3, q, k, ks, v, vs, table, [n], 0)
+    assert err == 0
+    check(E4M3, q, k, ks, v, vs, table, [n], out16, out32, lost(n))
+
+
+@pytest.mark.parametrize("P,HS,G", [(16, 128, 4), (32, 256, 16)])
+def test_v_scales_far_apart_in_any_order(P, HS, G):
+    """Scales from 2^-126 to 2^110, rising, falling and mixed, in bands of one share and of several."""
+    for order in ("rising", "falling", "mixed"):
+        for n in (300, 3000):
+            N = -(-n // P)
+            k, ks, _ = make_pool(E4M3, N, 1, P, HS, 3)
+            v, _, _ = make_pool(E4M3, N, 1, P, HS, 4)
+            e = torch.linspace(-126, 110, N).round()
+            e = e.flip(0) if order == "falling" else e[torch.randperm(N, generator=torch.Generator().manual_seed(n))] if order == "mixed" else e
+            table = np.arange(N, dtype=np.int32)[None]
+            q = _values((1, G, HS), 7).bfloat16()
+            vs = torch.exp2(e)[:, None].contiguous()
+            out16, out32, err = run_attn(E4M3, q, k, ks, v, vs, table, [n], 0)
+            assert err == 0
+            check(E4M3, q, k, ks, v, vs, table, [n], out16, out32, lost(n))
+
+
+def test_zeros_that_the_writer_stored():
+    """A prompt whose first 150 values are zero, written by fd_paged_append and attended to."""
+    B, NKV, G, HS, P, n = 1, 2, 4, 128, 16, 400
+    N = n // P
+    rows = _values((n, 2, NKV, HS), 3).bfloat16()
+    rows[:150, 1] = 0
+    rows[n - 1, 1, 0] = 0
+    k, v = (torch.full((N, NKV, P, HS), ref.NAN_CODE, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((N, NKV), float("nan"), device="cuda") for _ in range(2))
+    table, lens = np.arange(N, dtype=np.int32)[None], torch.tensor([n], dtype=torch.int32, device="cuda")
+    new = rows.cuda()
+    fd.fd_paged_append(new, new[:, 1], k, v, ks, vs, d(table), lens, torch.tensor([0, n], dtype=torch.int32, device="cuda"), None,
+                       B, n, NKV, HS, P, N, N, new.stride(0), new.stride(0), E4M3)
+    torch.cuda.synchronize()
+    assert (vs[:9].cpu() == 0).all()
+    q = _values((B, NKV * G, HS), 7).bfloat16()
+    k, ks, v, vs = (x.cpu() for x in (k, ks, v, vs))
+    out16, out32, err = run_attn(E4M3, q, k, ks, v, vs, table, [n], 0)
+    assert err == 0
+    check(E4M3, q, k, ks, v, vs, table, [n], out16, out32, lost(n))
