@@ -39,7 +39,7 @@
 // instead of 16 cost the tensor cores nothing here: an MMA takes as long as reading its
 // 128-row operand. Head dim 512 with 16 rows has tensor memory for 48 columns: the terms go there in pairs, both
 // unscaled in one column, by two MMAs one behind the other, pairs 256 apart (nothing is dropped above 2^-26).
-// bf16 takes q as it is and w = w0 + w1 (16 bits).
+// bf16 takes q as it is and w = w0 + w1 + w2 (24 bits).
 //
 // Scales. K's multiplies the score. V's multiplies the weight, in units of 2^vref, vref the exponent of the
 // largest V scale that the group has met in the segment: w_p = 2^(s_p log2(e) - m) * (vs / 2^vref), so that w fits
@@ -367,7 +367,7 @@ struct Cfg {
   static constexpr int SLOT = CH * CHUNK;
   static constexpr int KSTEP = 32 / EB;                // K of one MMA (32 bytes)
   static constexpr int QT = KV8 ? 2 : 1;               // terms of q
-  static constexpr int PT = KV8 ? 6 : 2;               // terms of a weight
+  static constexpr int PT = KV8 ? 6 : 3;               // terms of a weight
   static constexpr int PP = KV8 && HS * NQ > 4096 ? 2 : 1;  // terms that share a column
   static constexpr int NS = round16(QT * NQ);          // columns of S
   static constexpr int NP = round16(PT / PP * NQ);     // columns of O

@@ -107,7 +107,7 @@ int fd_paged_plan_sms(int B, int NH, int NKV, int HS, int page_size, int max_pag
  * 2^-30 of that, so n positions of weights that are that small may add n times
  * as much to the error); products accumulate in fp32. Every scale that is not
  * negative is taken, 0 and subnormals too. bf16: q enters as it
- * is, the weights as two bf16 terms (2^-16).
+ * is, the weights as three bf16 terms (2^-24).
  * fd_paged_attn makes its plan for the current device and uses a workspace
  * the library owns, one per (device, stream): the first call for a pair
  * allocates it (not while the stream is captured: FD_ERR_WORKSPACE), large

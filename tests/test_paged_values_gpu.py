@@ -26,7 +26,7 @@ def test_small_weights_behind_a_large_one(kv, HS, G, bits, n, sink, B):
     Bound: a score is one product, and its way to the weight has at most six roundings of a number below 32 (the two factors
     of the multiplier, the product, the reference, the difference) and exp2's two last places: 6 * 2^5 * 2^-24 * ln 2 + 2^-22
     < 2^-16 of the weight; six terms hold a weight to 2^-24 of itself or 2^-32 of the largest (2^-30 where terms share a
-    column: head dim 512, more than 8 rows; bf16 has no such floor), two bf16 terms to 2^-16;
+    column: head dim 512, more than 8 rows; bf16 has no such floor), three bf16 terms to 2^-24;
     the sums of n products, 32 an addition, are off by at most 2^-23 an addition."""
     P = 64
     N = -(-n // P)
@@ -64,11 +64,39 @@ def test_small_weights_behind_a_large_one(kv, HS, G, bits, n, sink, B):
     w = torch.exp(-part.double() * top)[:, None]
     want = w * flat.sum(0) / (1 + (n - 1) * w)
     floor = 0.0 if kv == BF16 else 2.0 ** -30 if HS == 512 and G > 8 else 2.0 ** -32
-    rel = 2.0 ** -16 + (n / 32 + 64) * 2.0 ** -23 + (2.0 ** -16 if kv == BF16 else 2.0 ** -24)
+    rel = 2.0 ** -16 + (n / 32 + 64) * 2.0 ** -23 + 2.0 ** -24
     lim = rel * want + n * floor * flat.max()
     err = (out32.double().cpu() - want).abs()
     assert (err <= lim).all(), f"{(err / lim).max():.2f} of the bound, {(err / want).max():.2e} of the output"
     assert ((out.double().cpu() - want).abs() <= lim + want * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("kv,HS,G", [(BF16, 64, 3), (BF16, 128, 8), (BF16, 512, 16), (E4M3, 64, 3), (E4M3, 128, 8),
+                                     (E4M3, 256, 16), (E4M3, 512, 16)])
+def test_weights_hold_24_bits(kv, HS, G):
+    """Two positions whose values are 0 and 1: the fp32 output is the second's weight over their sum.
+
+    Bound, relative to the output: a score is one product of at most 2 in size in powers of two, with at most six roundings on
+    its way to the weight (6 * 2 * 2^-24 * ln 2 = 2^-20.9) and exp2's two last places (2^-22); three roundings (the weight's terms,
+    the sum, the quotient) of 2^-24. Together below 2^-20; both weights take part, so twice that."""
+    P, B = 16, 40
+    k, v = torch.zeros(1, 1, P, HS), torch.zeros(1, 1, P, HS)
+    k[0, 0, 1, 0], v[0, 0, 1] = 1.0, 1.0
+    ks = vs = None
+    if kv == E4M3:
+        k, v = (x.to(torch.float8_e4m3fn).view(torch.uint8) for x in (k, v))
+        ks, vs = torch.ones(1, 1), torch.ones(1, 1)
+    else:
+        k, v = k.bfloat16(), v.bfloat16()
+    q = torch.zeros(B, G, HS)
+    q[:, :, 0] = 2 * torch.rand(B, G, generator=torch.Generator().manual_seed(HS + G)) - 1
+    q = q.bfloat16()
+    _, out32, err = run_attn(kv, q, k, ks, v, vs, np.zeros((B, 1), dtype=np.int32), [2] * B, 0, 1.0)
+    assert err == 0
+    w = torch.exp(q[:, :, :1].double())
+    want = w / (1 + w)
+    off = ((out32.double() - want) / want).abs().max().item()
+    assert off <= 2.0 ** -19, f"2^{math.log2(off):.1f}"
 
 
 def check(kv, q, k, ks, v, vs, table, lens, out16, out32, e2):
