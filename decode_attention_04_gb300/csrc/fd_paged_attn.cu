@@ -32,7 +32,9 @@
 //
 // E4M3 products are exact but for the other operand, which enters as a sum of
 // E4M3 terms, each in MMA columns of its own, term i scaled by 16^i so that it
-// has E4M3's full range: q = q0 + q1 / 16 (8 significant bits: all that bf16 has),
+// has E4M3's full range: q = q0 + q1 / 16 + q2 / 256 (bf16 has 8 significant bits, so elements down to 2^-17 of the row's
+// largest are exact and no other is off by more than 2^-25 of it; head dim 512 with 16 rows has two terms, 2^-13 and
+// 2^-21: a third takes 16 KB from the ring there, 4 x 131072 MQA 96.4 -> 97.8 us, 32768 positions 20.4 -> 21.5),
 // w = w0 + w1 / 16 + ... + w5 / 16^5 (24 bits, as many as the sum has, and nothing is dropped above 2^-30: with three
 // terms weights below 2^-18 were, which in a long band are the output where the largest weight's value is
 // small). The columns are added in fp32 at the end. 96 columns
@@ -366,9 +368,10 @@ struct Cfg {
   static constexpr int CHUNK = kTile * SW;
   static constexpr int SLOT = CH * CHUNK;
   static constexpr int KSTEP = 32 / EB;                // K of one MMA (32 bytes)
-  static constexpr int QT = KV8 ? 2 : 1;               // terms of q
+  static constexpr bool WIDE = KV8 && HS * NQ > 4096;  // head dim 512, 16 rows: the least shared and tensor memory a term
+  static constexpr int QT = !KV8 ? 1 : WIDE ? 2 : 3;   // terms of q
   static constexpr int PT = KV8 ? 6 : 3;               // terms of a weight
-  static constexpr int PP = KV8 && HS * NQ > 4096 ? 2 : 1;  // terms that share a column
+  static constexpr int PP = WIDE ? 2 : 1;              // of them in a column
   static constexpr int NS = round16(QT * NQ);          // columns of S
   static constexpr int NP = round16(PT / PP * NQ);     // columns of O
   static constexpr int COLS = pow2_cols(2 * NS + 2 * NB * NP);
@@ -743,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             const int sh = (top > 0.f && ex < 255) ? min(7 - (ex - 127), 126) : 0;
             const float mul = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
             if (pc == 0 && r < C::NQ) qmul[(t.seg & (kQRing - 1)) * 16 + r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-            uint32_t w[2][4];
+            uint32_t w[C::QT][4];
   #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float2 y = make_float2(f[i].x * mul, f[i].y * mul);
@@ -752,16 +755,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 y.x = isfinite(y.x) ? y.x : __int_as_float(0x7fffffff);
                 y.y = isfinite(y.y) ? y.y : __int_as_float(0x7fffffff);
               }
+              __half2 h = __floats2half2_rn(y.x, y.y);  // exact above 2^-17, else to 2^-25
   #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t term = next_term(y, 16.f);
+              for (int j = 0; j < C::QT; ++j) {
+                const uint32_t term = next_term(h, 16.f);
                 if (i & 1) w[j][i / 2] |= term << 16;
                 else w[j][i / 2] = term;
               }
             }
             if (r < C::NQ) {
   #pragma unroll
-              for (int j = 0; j < 2; ++j)
+              for (int j = 0; j < C::QT; ++j)
                 *reinterpret_cast<uint4*>(qb + chunk * C::NS * C::SW + swizzled<C::SW>(j * C::NQ + r, piece)) =
                     make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
             }
@@ -1068,8 +1072,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           const float4 m = qm[r / 4];
           const float mul[4] = {ksvs.x * m.x, ksvs.x * m.y, ksvs.x * m.z, ksvs.x * m.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            sc[r + j] = live ? (s[r + j] + s[C::NQ + r + j] * 0.0625f) * mul[j] : kNegInf;
+          for (int j = 0; j < 4; ++j) {
+            float low = s[C::NQ + r + j];
+            if constexpr (C::QT > 2) low += s[2 * C::NQ + r + j] * 0.0625f;
+            sc[r + j] = live ? (s[r + j] + low * 0.0625f) * mul[j] : kNegInf;
+          }
         }
       } else {
 #pragma unroll

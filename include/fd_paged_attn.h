@@ -100,8 +100,9 @@ int fd_paged_plan_sms(int B, int NH, int NKV, int HS, int page_size, int max_pag
  * An entry that names no page raises FD_DEVERR_PAGE_ID and its positions are
  * left out; len_b < 0 counts as 0 (FD_DEVERR_LEN_NEGATIVE); len_b above
  * max_pages * page_size counts as that (FD_DEVERR_LEN_CLAMPED).
- * Arithmetic, E4M3: q is split into two E4M3 terms (exact for elements within
- * 2^13 of the row's largest, else off by 2^-21 of that) and the softmax
+ * Arithmetic, E4M3: q is split into three E4M3 terms (exact for elements within
+ * 2^17 of the row's largest, else off by 2^-25 of that; HS 512 with NH / NKV > 8:
+ * two terms, 2^13 and 2^-21) and the softmax
  * weights, times their block's V scale, into six (off by 2^-24 of themselves or
  * 2^-32 of the largest weight times the largest scale; HS 512 with NH / NKV > 8:
  * 2^-30 of that, so n positions of weights that are that small may add n times

@@ -99,6 +99,39 @@ def test_weights_hold_24_bits(kv, HS, G):
     assert off <= 2.0 ** -19, f"2^{math.log2(off):.1f}"
 
 
+@pytest.mark.parametrize("kv,HS,G", [(BF16, 128, 4), (E4M3, 64, 3), (E4M3, 128, 8), (E4M3, 128, 16), (E4M3, 256, 12),
+                                     (E4M3, 512, 8), (E4M3, 512, 16)])
+def test_small_elements_of_q_beside_a_large_one(kv, HS, G):
+    """A query row whose largest element meets zeros in K; the others, 2^-13.3 of it, make the score, 2 at the second of two
+    positions, whose values are 0 and 1.
+
+    Bound, relative to the output: that of test_weights_hold_24_bits; the score's sum, 2 HS 2^-23; with two terms of q (head dim
+    512, more than 8 rows) 2 * 2^-21 of the largest element over the others."""
+    P, B, top, small = 16, 3, 128.0, 201 * 2.0 ** -14
+    k, v = torch.zeros(1, 1, P, HS), torch.zeros(1, 1, P, HS)
+    k[0, 0, 1, 1:], v[0, 0, 1] = 64.0, 1.0
+    want_k = 2 / (small * (HS - 1))
+    ks = vs = None
+    if kv == E4M3:
+        k, v = (x.to(torch.float8_e4m3fn).view(torch.uint8) for x in (k, v))
+        ks, vs = torch.full((1, 1), want_k / 64), torch.ones(1, 1)
+        each = 64 * float(ks)
+    else:
+        k[0, 0, 1, 1:] = want_k
+        k, v = k.bfloat16(), v.bfloat16()
+        each = float(k[0, 0, 1, 1])
+    q = torch.full((B, G, HS), small)
+    q[:, :, 0] = top
+    q = q.bfloat16()
+    assert float(q[0, 0, 1]) == small
+    _, out32, err = run_attn(kv, q, k, ks, v, vs, np.zeros((B, 1), dtype=np.int32), [2] * B, 0, 1.0)
+    assert err == 0
+    want = 1 / (1 + math.exp(-small * each * (HS - 1)))
+    rel = 2.0 ** -19 + 2 * HS * 2.0 ** -23 + (2 * 2.0 ** -21 * top / small if kv == E4M3 and HS == 512 and G > 8 else 0.0)
+    off = ((out32.double() - want) / want).abs().max().item()
+    assert off <= rel, f"2^{math.log2(off):.1f} against 2^{math.log2(rel):.1f}"
+
+
 def check(kv, q, k, ks, v, vs, table, lens, out16, out32, e2):
     """Against the 64-bit reference; e2 bounds what the weights and the sums lose, relative to the largest value of the row.
     Outputs below 2^-126 are multiples of fp32's least value: its half, 2^-150, is added, and bf16's, 2^-134."""
