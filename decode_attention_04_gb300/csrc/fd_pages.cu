@@ -672,7 +672,7 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   // One block for a unit's items where there are units enough: looking a unit up
   // costs a warp as much as an item of 16 tokens (8 prompts, 8 heads: two blocks
   // a unit 40.6 us).
-  const int rounds = (2 * a.NKV + kItems - 1) / kItems;
+  const int rounds = std::min((2 * a.NKV + kItems - 1) / kItems, 65535);  // a grid's y; blocks take several items each
   return launch(append_kernel<KV8, VPT, WPI>, dim3(static_cast<unsigned>(units), units >= 1024 ? 1 : rounds), kBlock, 1,
                 stream, a);
 }
