@@ -28,9 +28,9 @@
  *
  * Conventions beside those of fd_decode_attn.h:
  *   - page_size is 16, 32, 64 or 128; HS is 64, 128, 256 or 512;
- *     max_pages * page_size is below 2^31 - 4096, and fd_paged_attn and
- *     fd_paged_append take at most 2^35 positions in all, B * max_pages *
- *     page_size (else FD_ERR_UNSUPPORTED).
+ *     max_pages * page_size is at most 2^31 - 4097, and for fd_paged_attn and
+ *     fd_paged_append B * (max_pages * page_size / 32 + 32) is below 2^31: close
+ *     to 2^36 positions in all (else FD_ERR_UNSUPPORTED).
  *   - Tensors are densely packed but for k_new and v_new of fd_paged_append,
  *     whose rows (tokens) may be any multiple of 8 elements apart.
  *   - q, out, the pages, k_new, v_new and workspaces are 16-byte aligned; the

@@ -10,6 +10,32 @@ BF16, E4M3 = fd.FD_KV_BF16, fd.FD_KV_E4M3
 DEV = "cuda"
 
 
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from decode_attention_04_gb300 import build
+    build.build()
+    return fd.load_library()
+
+
+@pytest.mark.parametrize("B,P,wide", [(32768, 32, 65504), (32768, 16, 131008), (65535, 128, 8185), (1, 16, 134217472)])
+def test_bound_on_positions(B, P, wide):
+    """B * (max_pages * page_size / 32 + 32) is below 2^31 and max_pages * page_size at most 2^31 - 4097: one page less than
+    each of these is taken, each is refused. The writer, given no token, shows the same bound."""
+    per = wide * P
+    assert B * (per // 32 + 32) >= 2 ** 31 or per > 2 ** 31 - 4097
+    assert B * ((per - P) // 32 + 32) < 2 ** 31 and per - P <= 2 ** 31 - 4097
+
+    def append(pages):
+        fd.fd_paged_append(*[None] * 8, 16, None, B, 0, 1, 64, P, 1, pages, 64, 64, BF16, 0)
+
+    assert fd.fd_paged_plan_sms(B, 2, 1, 64, P, wide - 1, 0, 152, BF16).max_pages == wide - 1
+    append(wide - 1)
+    for call in (lambda: fd.fd_paged_plan_sms(B, 2, 1, 64, P, wide, 0, 152, BF16), lambda: append(wide)):
+        with pytest.raises(fd.FdError) as e:
+            call()
+        assert e.value.status == fd.FD_ERR_UNSUPPORTED
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv", [BF16, E4M3], ids=["bf16", "e4m3"])
 def test_append_more_heads_than_a_grid_is_high(kv):
