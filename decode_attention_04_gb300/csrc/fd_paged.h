@@ -54,9 +54,9 @@ cudaError_t launch_pages_fork(const int* table, const int* lens, const int* pare
 cudaError_t launch_pages_free(int* table, int* lens, int* refs, const int* keep, int window, int B, int max_pages,
                               int num_pages, int P, cudaStream_t stream);
 cudaError_t launch_pages_compact(int* table, int* refs, int* moves, int* ws, int B, int max_pages, int num_pages,
-                                 cudaStream_t stream);
+                                 int sms, cudaStream_t stream);
 cudaError_t launch_pages_copy(void* k, void* v, float* ks, float* vs, const int* moves, int room, int layers,
-                              int num_pages, int NKV, size_t page_bytes, cudaStream_t stream);
+                              int num_pages, int NKV, size_t page_bytes, int sms, cudaStream_t stream);
 
 // The device error words of the paged units (OR into *err, then clear).
 cudaError_t read_and_clear_device_error_paged(unsigned int* err);

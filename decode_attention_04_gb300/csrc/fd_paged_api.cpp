@@ -144,6 +144,11 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 int status(cudaError_t e) { return e == cudaSuccess ? FD_OK : FD_ERR_CUDA; }
 
+int current_sms(int* sms) {
+  int device = 0;
+  return cudaGetDevice(&device) == cudaSuccess ? fd::device_sm_count(device, sms) : FD_ERR_CUDA;
+}
+
 }  // namespace
 
 namespace fd {
@@ -355,12 +360,15 @@ int fd_pages_free(int* table, int* lens, int* refs, const int* keep, int window,
 
 int fd_pages_compact(int* table, int* refs, int* moves, void* workspace, size_t workspace_bytes, int B, int max_pages,
                      int num_pages, fd_stream_t stream) {
-  const int rc = check_book(B, max_pages, num_pages);
+  int rc = check_book(B, max_pages, num_pages);
   if (rc != FD_OK) return rc;
   if (!refs || !moves || (B > 0 && !table)) return FD_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < fd_pages_workspace_bytes(B, num_pages)) return FD_ERR_WORKSPACE;
   if (!aligned(workspace, 16) || !aligned(table, 4) || !aligned(refs, 4) || !aligned(moves, 4)) return FD_ERR_ALIGNMENT;
-  return status(fd::launch_pages_compact(table, refs, moves, static_cast<int*>(workspace), B, max_pages, num_pages,
+  int sms = 0;
+  rc = current_sms(&sms);
+  if (rc != FD_OK) return rc;
+  return status(fd::launch_pages_compact(table, refs, moves, static_cast<int*>(workspace), B, max_pages, num_pages, sms,
                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -376,8 +384,11 @@ int fd_pages_copy(void* k_pages, void* v_pages, float* k_scale, float* v_scale, 
       (kv8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
     return FD_ERR_ALIGNMENT;
   const size_t page_bytes = static_cast<size_t>(NKV) * page_size * HS * (kv8 ? 1 : 2);
+  int sms = 0;
+  const int rc = current_sms(&sms);
+  if (rc != FD_OK) return rc;
   return status(fd::launch_pages_copy(k_pages, v_pages, kv8 ? k_scale : nullptr, kv8 ? v_scale : nullptr, moves, room,
-                                      layers, num_pages, NKV, page_bytes, reinterpret_cast<cudaStream_t>(stream)));
+                                      layers, num_pages, NKV, page_bytes, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

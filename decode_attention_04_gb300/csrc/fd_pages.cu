@@ -719,25 +719,25 @@ cudaError_t launch_pages_free(int* table, int* lens, int* refs, const int* keep,
 }
 
 cudaError_t launch_pages_compact(int* table, int* refs, int* moves, int* ws, int B, int max_pages, int num_pages,
-                                 cudaStream_t stream) {
+                                 int sms, cudaStream_t stream) {
   const bool one = num_pages <= kOneBlockPages;
   const cudaError_t e = launch(one ? compact_kernel<1> : compact_kernel<kCluster>, dim3(one ? 1 : kCluster), kBookThreads,
                                one ? 1 : kCluster, stream, refs, moves, ws, num_pages);
   const long long entries = static_cast<long long>(B) * max_pages;
   if (e != cudaSuccess || entries == 0) return e;
-  const unsigned blocks = static_cast<unsigned>(std::min((entries + kTableThreads - 1) / kTableThreads, 152ll * 8));
+  const unsigned blocks = static_cast<unsigned>(std::min((entries + kTableThreads - 1) / kTableThreads, sms * 8ll));
   return launch(renumber_kernel, dim3(blocks), kTableThreads, 1, stream, table, moves, ws, entries, num_pages);
 }
 
 cudaError_t launch_pages_copy(void* k, void* v, float* ks, float* vs, const int* moves, int room, int layers,
-                              int num_pages, int NKV, size_t page_bytes, cudaStream_t stream) {
+                              int num_pages, int NKV, size_t page_bytes, int sms, cudaStream_t stream) {
   const int pieces = static_cast<int>((page_bytes + kCopyPiece - 1) / kCopyPiece);
   const long long items = static_cast<long long>(room) * layers * 2 * pieces;
   // Two waves of the eight blocks that an SM holds: blocks do not all copy at one rate, and the second
-  // wave goes to the SMs that are ahead. Free, compact and copy of 230 MB with 8 / 16 / 24 / 32 / 64
+  // wave goes to the SMs that are ahead. On 152 SMs, free, compact and copy of 230 MB with 8 / 16 / 24 / 32 / 64
   // blocks an SM: 87.6 / 83.6 / 82.7 / 81.7 / 81.2 us; a beam step, whose list is nearly empty, with as
   // many blocks to start for nothing: 10.7 / 11.1 / 12.3 / 13.5 / 15.3 us.
-  const unsigned blocks = static_cast<unsigned>(std::min(items, 152ll * 16));
+  const unsigned blocks = static_cast<unsigned>(std::min(items, sms * 16ll));
   return launch(copy_kernel, dim3(blocks), kCopyThreads, 1, stream, static_cast<uint4*>(k), static_cast<uint4*>(v), ks,
                 vs, moves, room, layers, num_pages, NKV, page_bytes / 16, pieces);
 }
