@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import decode_attention_04_gb300 as fd
+from test_paged_gpu import case, empty
 
 BF16, E4M3 = fd.FD_KV_BF16, fd.FD_KV_E4M3
 DEV = "cuda"
@@ -62,3 +63,67 @@ def test_append_more_heads_than_a_grid_is_high(kv):
             x = (x.float() / s.float()[:, None, None]).to(torch.float8_e4m3fn).view(torch.uint8)
         assert torch.equal(pools[i][0, :, :T].view(torch.uint8), x.contiguous().view(torch.uint8))
         assert not pools[i][0, :, T:].view(torch.uint8).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("B", [128, 129, 1024, 1025, 3001])
+def test_attn_many_sequences(kv, B):
+    """On both sides of 128 sequences (a warp finds its share by itself) and of 1024 (lengths are kept in shared memory)."""
+    lens = [int(x) for x in np.random.default_rng(B).integers(0, 60, B)]
+    case(kv, 64, 1, 2, 16, lens, seed=B)
+    case(kv, 64, 2, 1, 16, [max(n - 20, 0) for n in lens], window=13, seed=B)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1500, 20000])
+@pytest.mark.parametrize("B", [1024, 1025, 2500])
+def test_bookkeeping_many_sequences(B, N):
+    """More than 1024 sequences: their lists lie in the workspace and are made in chunks of 1024, whose pages, grants and moves
+    go on from one to the next; in one block and in a cluster."""
+    P, rng = 16, np.random.default_rng(B + N)
+    dev = empty(B, 8, N, P)
+    fd.fd_get_device_error()
+    dev.reserve(rng.integers(-1, 4, B))               # with 1500 pages some sequences of a later chunk get none
+    dev.reserve(None)
+    dev.fork(rng.integers(0, B, B))                   # shared last pages in every chunk
+    _, moves = dev.reserve(rng.integers(0, 3, B))
+    assert N < 2 * B or len(moves) > 100
+    dev.free(rng.integers(0, 8, B))
+    dev.compact()
+    dev.reserve(rng.integers(0, 40, B))               # denied from the middle of a chunk on, where pages run out
+    dev.fork(rng.integers(-1, B, B + 3))
+    dev.free(None, 5)
+    dev.compact()
+    assert fd.fd_get_device_error() & fd.FD_DEVERR_PAGE_ID == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [1, 130])
+def test_attn_one_sequence_of_more_than_two_billion_pieces(B):
+    """2^31 pieces of 32 positions in one sequence (65535 heads, each of a band of 2^20 positions over the same four pages):
+    shares begin behind 2^31. Attention over pages that repeat is attention over them once. The other sequences are empty."""
+    NKV, HS, P, n = 65535, 64, 16, 1 << 20
+    assert NKV * (n // 32 + 16) > 2 ** 31
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    k, v = (torch.randn(4, NKV, P, HS, generator=gen, device=DEV).to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.ones(4, NKV, device=DEV) for _ in range(2))
+    q = torch.randn(B, NKV, HS, generator=gen, device=DEV).bfloat16()
+    table = torch.zeros(B, n // P, dtype=torch.int32, device=DEV)
+    table[B - 1] = torch.arange(n // P, device=DEV) % 4
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+    lens[B - 1] = n
+    out = torch.full_like(q, float("nan"))
+    fd.fd_get_device_error()
+    fd.paged_attention(q, k, v, table, lens, k_scale=ks, v_scale=vs, out=out)
+    assert fd.fd_get_device_error() == 0
+    assert not out[:B - 1].any()
+    for h in range(0, NKV, 4096):
+        kk, vv = (x[:, h:h + 4096].double().transpose(0, 1).reshape(-1, 4 * P, HS) for x in (k, v))
+        qq = q[B - 1, h:h + 4096].double()[:, None]
+        s = (qq @ kk.transpose(1, 2)) * HS ** -0.5
+        want = (torch.softmax(s, 2) @ vv)[:, 0]
+        mass = (qq.abs() @ kk.abs().transpose(1, 2)).amax(2) * HS ** -0.5
+        # the score's sum, weights of 24 bits, the sums over n positions (32 an addition, in two groups), and bf16's half step
+        lim = (4 * HS * 2.0 ** -23 * mass + 2.0 ** -20 + (n / 64) * 2.0 ** -23) * vv.abs().amax((1, 2))[:, None]
+        assert ((out[B - 1, h:h + 4096].double() - want).abs() <= lim + want.abs() * 2.0 ** -8).all()
