@@ -7,7 +7,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
-#include <utility>
+#include <tuple>
 
 #include <cuda_runtime.h>
 
@@ -79,7 +79,7 @@ int make_plan(int B, int NH, int NKV, int HS, int page_size, int max_pages, int 
 
 std::mutex g_mu;
 std::map<int, int> g_sms;
-std::map<std::pair<int, uintptr_t>, void*> g_ws;
+std::map<std::tuple<int, uintptr_t, unsigned long long>, void*> g_ws;  // device, stream, its id where the handle is shared
 
 int run(const fd_paged_plan_t& p, void* workspace, size_t workspace_bytes, float* out_f32, const void* q,
         const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale, void* out,
@@ -171,9 +171,12 @@ int device_sm_count(int device, int* sms) try {
 
 // One buffer per (device, stream), large enough for every shape on that device, so
 // it never grows and a captured graph's pointer stays good until fd_release.
+// The handle of the per-thread default stream names another stream in each thread.
 int paged_workspace(int device, cudaStream_t stream, size_t bytes, void** ptr) try {
+  unsigned long long id = 0;
+  if (stream == cudaStreamPerThread && cudaStreamGetId(stream, &id) != cudaSuccess) return FD_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
-  void*& w = g_ws[{device, reinterpret_cast<uintptr_t>(stream)}];
+  void*& w = g_ws[{device, reinterpret_cast<uintptr_t>(stream), id}];
   if (!w) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return FD_ERR_CUDA;
@@ -195,7 +198,7 @@ void paged_release() {
     if (!kv.second) continue;
     int prev = 0;
     cudaGetDevice(&prev);
-    cudaSetDevice(kv.first.first);
+    cudaSetDevice(std::get<0>(kv.first));
     cudaFree(kv.second);
     cudaSetDevice(prev);
   }

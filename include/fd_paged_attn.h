@@ -110,7 +110,8 @@ int fd_paged_plan_sms(int B, int NH, int NKV, int HS, int page_size, int max_pag
  * negative is taken, 0 and subnormals too. bf16: q enters as it
  * is, the weights as three bf16 terms (2^-24).
  * fd_paged_attn makes its plan for the current device and uses a workspace
- * the library owns, one per (device, stream): the first call for a pair
+ * the library owns, one per (device, stream; the per-thread default stream is a
+ * stream of its own in each thread): the first call for a pair
  * allocates it (not while the stream is captured: FD_ERR_WORKSPACE), large
  * enough for every shape, and it is kept until fd_release, so graphs captured
  * on one stream share it and must not be replayed at the same time.

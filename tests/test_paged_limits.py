@@ -1,4 +1,6 @@
-"""The paged cache at the ends of its ranges: many heads, many sequences, the largest batches of positions."""
+"""The paged cache at the ends of its ranges: many heads, many sequences, the largest batches of positions, several threads."""
+
+import threading
 
 import numpy as np
 import pytest
@@ -127,3 +129,36 @@ def test_attn_one_sequence_of_more_than_two_billion_pieces(B):
         # the score's sum, weights of 24 bits, the sums over n positions (32 an addition, in two groups), and bf16's half step
         lim = (4 * HS * 2.0 ** -23 * mass + 2.0 ** -20 + (n / 64) * 2.0 ** -23) * vv.abs().amax((1, 2))[:, None]
         assert ((out[B - 1, h:h + 4096].double() - want).abs() <= lim + want.abs() * 2.0 ** -8).all()
+
+
+@pytest.mark.gpu
+def test_threads_on_their_default_streams_have_a_workspace_each():
+    """The per-thread default stream has one handle (2) for as many streams as there are threads, which may run at the same
+    time: the library's workspace (10 MB on 152 SMs) is allocated for each."""
+    P, HS, n = 16, 128, 4000
+    k = torch.randn(n // P, 2, P, HS, device=DEV).bfloat16()
+    q = torch.randn(1, 8, HS, device=DEV).bfloat16()
+    table = torch.arange(n // P, dtype=torch.int32, device=DEV)[None]
+    lens = torch.full((1,), n, dtype=torch.int32, device=DEV)
+    want = fd.paged_attention(q, k, k, table, lens)
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    torch.cuda.synchronize()
+    free, failed = [torch.cuda.mem_get_info()[0]], []
+
+    def call(out):
+        try:
+            torch.cuda.set_device(q.device)
+            for _ in range(2):
+                fd.fd_paged_attn(q, k, k, None, None, out, table, lens, 1, 8, 2, HS, P, n // P, n // P, 0, 0.0, BF16, 2)
+            torch.cuda.synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    for out in outs:
+        t = threading.Thread(target=call, args=(out,))
+        t.start()
+        t.join()
+        free.append(torch.cuda.mem_get_info()[0])
+    assert not failed
+    assert free[0] - free[1] >= 9 << 20 and free[1] - free[2] >= 9 << 20
+    assert all(torch.equal(out.view(torch.int16), want.view(torch.int16)) for out in outs)
