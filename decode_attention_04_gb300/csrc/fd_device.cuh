@@ -1,7 +1,8 @@
-// Device-side helpers shared by the split kernels (fd_kernels.cu, fd_umma.cu):
-// the band and chunk rules, bf16 bit conversions, mbarrier waits that give up
-// after about a second, bulk copies, programmatic dependent launch, cluster
-// and proxy fences. Included inside `namespace fd { namespace { ... } }`, so
+// Device-side helpers shared by the kernels of the contiguous cache
+// (fd_kernels.cu, fd_umma.cu) and of the cache in pages (fd_paged_attn.cu,
+// fd_pages.cu): the band and chunk rules, bf16 bit conversions, mbarrier waits
+// that give up after about a second, bulk copies, programmatic dependent
+// launch, cluster and proxy fences. Included inside `namespace fd { namespace { ... } }`, so
 // every translation unit gets its own copy, including its own device error
 // word `g_device_error` (read back by that unit's host code).
 #pragma once

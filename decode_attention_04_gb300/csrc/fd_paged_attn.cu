@@ -66,91 +66,9 @@ namespace fd {
 namespace {
 
 #include "fd_device.cuh"
+#include "fd_tcgen05.cuh"
 
 // ------------------------------------------------------------- PTX helpers
-
-__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-               : "memory");
-}
-
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// D (tensor memory) = A * B (+ D when accumulate != 0), one thread issues.
-template <bool KV8>
-__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                     uint32_t accumulate) {
-  if constexpr (KV8) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  }
-}
-
-// The mbarrier gets one arrival when every MMA this thread issued so far has
-// completed (and stopped reading its shared-memory operands).
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// 16 consecutive 32-bit columns of this warp's 32 tensor-memory lanes; the
-// values are there after tmem_ld_wait.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-// N columns (a multiple of 16), waited for.
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
-  uint32_t r[N];
-#pragma unroll
-  for (int i = 0; i < N; i += 16) tmem_ld16(taddr + i, r + i);
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    asm volatile("" : "+r"(r[i]));  // no use before the wait
-    v[i] = __uint_as_float(r[i]);
-  }
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
-      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
-      "r"(__float_as_uint(v[15]))
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 3-D TMA tile load (x = head dim, y = head and slot of a page, z = page).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -159,10 +77,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "[%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
-}
-
-__device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap* m) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
 // Shared-memory matrix descriptor: start address / 16 in bits 0-13, leading
@@ -408,13 +322,6 @@ struct Cfg {
                                        (static_cast<uint32_t>(NP >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 };
 
-struct MaxOp {
-  __device__ float operator()(float x, float y) const { return fmaxf(x, y); }
-};
-struct AddOp {
-  __device__ float operator()(float x, float y) const { return x + y; }
-};
-
 // Reduction of N per-thread values (one per query row) over the 32 lanes of a
 // warp by halving: each exchange hands half of the rows still held to the
 // partner lane. Lane l ends with row l / (32 / N).
@@ -467,7 +374,8 @@ __device__ __forceinline__ uint16_t next_term(__half2& x, float by) {
 // holds what is left (its first 11 bits, after four terms the rest): half as many instructions as in fp32.
 template <int PP>
 __device__ __forceinline__ void six_terms(float2 w, uint16_t (&c)[6]) {
-  constexpr float kLast = PP == 1 ? 16.f : 256.f, kFirst = PP == 1 ? 16.f : 1.f;  // behind the terms that end a column, the others
+  // behind the terms that end a column, and behind the others
+  constexpr float kLast = PP == 1 ? 16.f : 256.f, kFirst = PP == 1 ? 16.f : 1.f;
   __half2 x = __floats2half2_rn(w.x, w.y);
   const float2 hi = __half22float2(x);
   c[0] = next_term(x, kFirst);
@@ -507,7 +415,8 @@ struct Cut {
 // The smallest power of the running reference that is moved: 2^(s - m) is at most 2^(kLazy + kBias). E4M3: that is
 // 2^7, and V's scale in units of 2^vref is below 2, which keeps weights within E4M3's 448. A higher bias leaves
 // smaller weights above what the terms drop, a lower one moves the reference less often: terms with a column each drop
-// less and take the lower one (3 / 4 / 5 before a move: ragged batch E4M3 107 / 106 / 105 us, 4 x 131072 MQA 97.7 / 97.6 / 97.6).
+// less and take the lower one (a move at 2^3 / 2^4 / 2^5: ragged batch E4M3 107 / 106 / 105 us, 4 x 131072 MQA 97.7 /
+// 97.6 / 97.6, both before the issue loops were rolled).
 constexpr float kTop8 = 7.f, kLazy8 = 5.f, kLazy8Shared = 3.f;
 constexpr float kLazy16 = 8.f, kBias16 = 0.f;
 
@@ -709,70 +618,72 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   int slots_used = 0;  // of the ring of a copy warp
 
   // Query rows of a segment -> the B operand of its score MMAs: rows of SW bytes, swizzled,
-      // term j of row r in row j * NQ + r; rows >= G are zero.
-      auto stage_q = [&](const Tile& t, int first, int threads) {
-        const int par = t.seg & 1;
-        unsigned char* qb = smem + C::OFF_Q + par * C::Q_STRIDE;
-        constexpr int EL = 16 / C::EB;           // elements of a 16-byte piece
-        constexpr int PIECES = C::HS / EL;       // of a row: a power of two, at most 64
-        for (int id = first; (id & ~31) < C::NQ * PIECES; id += threads) {  // whole warps
-          const int r = id / PIECES, pc = id % PIECES;
-          const bool live = r < G && r < C::NQ;
-          const int chunk = pc * 16 / C::SW, piece = (pc * 16 % C::SW) / 16;
-          const uint16_t* src = a.q + (static_cast<size_t>(t.b) * a.NH + static_cast<size_t>(t.kvh) * G + r) * C::HS + pc * EL;
-          if constexpr (!C::KV8) {
-            if (r < C::NQ)
-              *reinterpret_cast<uint4*>(qb + chunk * C::NS * C::SW + swizzled<C::SW>(r, piece)) =
-                  live ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
-          } else {
-            uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            if (live) {
-              x[0] = reinterpret_cast<const uint4*>(src)[0];
-              x[1] = reinterpret_cast<const uint4*>(src)[1];
-            }
-            const uint32_t* u = reinterpret_cast<const uint32_t*>(x);
-            float2 f[8];
-            float top = 0.f;
-  #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
-              top = fmaxf(top, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
-            }
-            // the row's largest element, over the lanes that hold the row
-  #pragma unroll
-            for (int i = PIECES / 2; i >= 1; i /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-            // times a power of two that brings it to [128, 256); not finite: as it is
-            const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // biased exponent of top >= 0
-            const int sh = (top > 0.f && ex < 255) ? min(7 - (ex - 127), 126) : 0;
-            const float mul = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-            if (pc == 0 && r < C::NQ) qmul[(t.seg & (kQRing - 1)) * 16 + r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-            uint32_t w[C::QT][4];
-  #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float2 y = make_float2(f[i].x * mul, f[i].y * mul);
-              // an infinity would saturate: it has to reach the scores as NaN
-              if (ex == 255) {
-                y.x = isfinite(y.x) ? y.x : __int_as_float(0x7fffffff);
-                y.y = isfinite(y.y) ? y.y : __int_as_float(0x7fffffff);
-              }
-              __half2 h = __floats2half2_rn(y.x, y.y);  // exact above 2^-17, else to 2^-25
-  #pragma unroll
-              for (int j = 0; j < C::QT; ++j) {
-                const uint32_t term = next_term(h, 16.f);
-                if (i & 1) w[j][i / 2] |= term << 16;
-                else w[j][i / 2] = term;
-              }
-            }
-            if (r < C::NQ) {
-  #pragma unroll
-              for (int j = 0; j < C::QT; ++j)
-                *reinterpret_cast<uint4*>(qb + chunk * C::NS * C::SW + swizzled<C::SW>(j * C::NQ + r, piece)) =
-                    make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
-            }
+  // term j of row r in row j * NQ + r; rows >= G are zero.
+  auto stage_q = [&](const Tile& t, int first, int threads) {
+    const int par = t.seg & 1;
+    unsigned char* qb = smem + C::OFF_Q + par * C::Q_STRIDE;
+    constexpr int EL = 16 / C::EB;           // elements of a 16-byte piece
+    constexpr int PIECES = C::HS / EL;       // of a row: a power of two, at most 64
+    for (int id = first; (id & ~31) < C::NQ * PIECES; id += threads) {  // whole warps
+      const int r = id / PIECES, pc = id % PIECES;
+      const bool live = r < G && r < C::NQ;
+      const int chunk = pc * 16 / C::SW, piece = (pc * 16 % C::SW) / 16;
+      const size_t row = static_cast<size_t>(t.b) * a.NH + static_cast<size_t>(t.kvh) * G + r;
+      const uint16_t* src = a.q + row * C::HS + pc * EL;
+      if constexpr (!C::KV8) {
+        if (r < C::NQ)
+          *reinterpret_cast<uint4*>(qb + chunk * C::NS * C::SW + swizzled<C::SW>(r, piece)) =
+              live ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+      } else {
+        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (live) {
+          x[0] = reinterpret_cast<const uint4*>(src)[0];
+          x[1] = reinterpret_cast<const uint4*>(src)[1];
+        }
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(x);
+        float2 f[8];
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+          top = fmaxf(top, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
+        }
+        // the row's largest element, over the lanes that hold the row
+#pragma unroll
+        for (int i = PIECES / 2; i >= 1; i /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+        // times a power of two that brings it to [128, 256); not finite: as it is
+        const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // biased exponent of top >= 0
+        const int sh = (top > 0.f && ex < 255) ? min(7 - (ex - 127), 126) : 0;
+        const float mul = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+        if (pc == 0 && r < C::NQ)
+          qmul[(t.seg & (kQRing - 1)) * 16 + r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+        uint32_t w[C::QT][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float2 y = make_float2(f[i].x * mul, f[i].y * mul);
+          // an infinity would saturate: it has to reach the scores as NaN
+          if (ex == 255) {
+            y.x = isfinite(y.x) ? y.x : __int_as_float(0x7fffffff);
+            y.y = isfinite(y.y) ? y.y : __int_as_float(0x7fffffff);
+          }
+          __half2 h = __floats2half2_rn(y.x, y.y);  // exact above 2^-17, else to 2^-25
+#pragma unroll
+          for (int j = 0; j < C::QT; ++j) {
+            const uint32_t term = next_term(h, 16.f);
+            if (i & 1) w[j][i / 2] |= term << 16;
+            else w[j][i / 2] = term;
           }
         }
-        fence_proxy_async_smem();
-      };
+        if (r < C::NQ) {
+#pragma unroll
+          for (int j = 0; j < C::QT; ++j)
+            *reinterpret_cast<uint4*>(qb + chunk * C::NS * C::SW + swizzled<C::SW>(j * C::NQ + r, piece)) =
+                make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+  };
 
   // ---------------------------------------------------------------- copy warps
   auto copy_tiles = [&] {
@@ -848,16 +759,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         if (lane == 1) bar = s_free + 8 * g, want = ((i >> 1) - 1) & 1;
         if (lane == 2) bar = q_ready + 8 * par, want = (walk.t.seg >> 1) & 1;
         wait_lanes(bar, want, lane == 0 || (lane == 1 && i >= 2) || (lane == 2 && walk.t.j == 0), failed);
-  #pragma unroll 1
+#pragma unroll 1
         for (int p = 0; p < C::NB; ++p) {
           if (p > 0) warp_wait(full + 8 * slot, turn, failed);
           tc_fence_after();
           if (issuer) {
             const uint64_t qp = qd + p * ((C::CH * C::NS * C::SW) >> 4);
             const uint64_t kd = k_desc + static_cast<uint32_t>(slot) * (C::SLOT >> 4);
-  #pragma unroll
+#pragma unroll
             for (int ch = 0; ch < C::CH; ++ch)
-  #pragma unroll
+#pragma unroll
               for (int kk = 0; kk < C::SW / 32; ++kk)
                 umma<C::KV8>(d, kd + ((ch * C::CHUNK + 32 * kk) >> 4),
                              qp + ((ch * C::NS * C::SW + 32 * kk) >> 4), C::IDESC_QK, (p | ch | kk) != 0);
@@ -903,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const uint64_t pd = p_desc + g * (C::P_BYTES >> 4);
         const int nk = (min(kTile, walk.t.end - walk.t.pos) + C::KSTEP - 1) / C::KSTEP;
         const uint32_t keep = takes ? 0u : 1u;
-  #pragma unroll 1
+#pragma unroll 1
         for (int p = 0; p < C::NB; ++p) {
           if (p > 0) warp_wait(full + 8 * slot, turn, failed);
           if (clear) {  // the group clears rows of the slot first
@@ -1436,18 +1347,6 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
 }
 
 // ------------------------------------------------------------------ the launch
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
 
 // A pool as a 3-D tensor (head dim; head and slot; page), read in boxes of one
 // swizzle width x `box_rows` rows of one page.

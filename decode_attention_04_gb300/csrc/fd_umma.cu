@@ -52,6 +52,7 @@ namespace fd {
 namespace {
 
 #include "fd_device.cuh"
+#include "fd_tcgen05.cuh"
 
 namespace um {
 constexpr int HS = 512;                   // head dim
@@ -119,75 +120,6 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uin
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-               : "memory");
-}
-
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// D (tensor memory) = A * B (+ D when accumulate != 0), one thread issues.
-__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The mbarrier gets one arrival when every MMA this thread issued so far has
-// completed (and stopped reading its shared-memory operands).
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
-}
-
-// 16 consecutive 32-bit columns of this warp's 32 tensor-memory lanes (one
-// lane per thread), waited for before returning.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
-      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
-      "r"(__float_as_uint(v[15]))
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 // Transaction bytes a phase of the barrier will receive, without an arrival
 // (the arrival comes after the copy warp's own stores into the same stage).
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
@@ -201,10 +133,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
-}
-
-__device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap* m) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
 // Row reduction of 16 per-thread values (one per query row) over the 32 lanes
@@ -227,13 +155,6 @@ __device__ __forceinline__ float rowreduce16(const float (&v)[16], int lane, Op 
   const float a1 = op(u1 ? a2[1] : a2[0], __shfl_xor_sync(0xffffffffu, u1 ? a2[0] : a2[1], 2));
   return op(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
 }
-
-struct MaxOp {
-  __device__ float operator()(float x, float y) const { return fmaxf(x, y); }
-};
-struct AddOp {
-  __device__ float operator()(float x, float y) const { return x + y; }
-};
 
 struct UmmaMaps {
   CUtensorMap k[um::NMAP], v[um::NMAP];  // boxes of 64 dims x 128, 64, 32, 16, 8 rows
@@ -449,7 +370,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
               const uint32_t qb = base + OFF_Q + c * ATOM_Q;
 #pragma unroll
               for (int kk = 0; kk < DC / 16; ++kk)
-                umma_bf16(tmem + 16 * (kt & 1), sw128_desc(kb + h * CHUNK_BYTES + 32 * kk, 16, 1024),
+                umma<false>(tmem + 16 * (kt & 1), sw128_desc(kb + h * CHUNK_BYTES + 32 * kk, 16, 1024),
                           sw128_desc(qb + 32 * kk, 16, 1024), kIdescQK, (c | kk) != 0);
             }
             umma_commit(empty + 8 * slot);
@@ -474,8 +395,8 @@ __global__ void __launch_bounds__(um::THREADS, 1)
             for (int kk = 0; kk < nk; ++kk) {
               const uint64_t adesc = sw128_desc(vb + kk * 2048, CHUNK_BYTES, 1024);
               const uint32_t patom = pb + (kk >> 2) * ATOM_Q + (kk & 3) * 32;
-              umma_bf16(d, adesc, sw128_desc(patom, 16, 1024), kIdescPV, (vt > 0 || kk > 0) ? 1u : 0u);
-              umma_bf16(d, adesc, sw128_desc(patom + P_HALF, 16, 1024), kIdescPV, 1u);
+              umma<false>(d, adesc, sw128_desc(patom, 16, 1024), kIdescPV, (vt > 0 || kk > 0) ? 1u : 0u);
+              umma<false>(d, adesc, sw128_desc(patom + P_HALF, 16, 1024), kIdescPV, 1u);
             }
             umma_commit(empty + 8 * slot);
             if (++vp == NPAIR) {
@@ -546,7 +467,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
       mbar_wait(s_full + 8 * (i & 1), (i >> 1) & 1, failed);
       tc_fence_after();
       float sc[NQ];
-      tmem_ld16(tmem + tlane + 16 * (i & 1), sc);
+      tmem_load<16>(tmem + tlane + 16 * (i & 1), sc);
       tc_fence_before();
       mbar_arrive(s_free + 8 * (i & 1));  // S(i) read: its buffer may take S(i + 2)
       const bool valid = pl < nv;
@@ -579,7 +500,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
 #pragma unroll
           for (int mb = 0; mb < NCH / 2; ++mb) {
             float o[NQ];
-            tmem_ld16(tmem + tlane + 32 + 16 * mb, o);
+            tmem_load<16>(tmem + tlane + 32 + 16 * mb, o);
 #pragma unroll
             for (int r = 0; r < NQ; ++r) o[r] *= alpha[r];
             tmem_st16(tmem + tlane + 32 + 16 * mb, o);
@@ -630,7 +551,7 @@ __global__ void __launch_bounds__(um::THREADS, 1)
 #pragma unroll
     for (int mb = 0; mb < NCH / 2; ++mb) {
       float o[NQ];
-      tmem_ld16(tmem + tlane + 32 + 16 * mb, o);
+      tmem_load<16>(tmem + tlane + 32 + 16 * mb, o);
       const int d = mb * 128 + quarter * 32 + lane;  // O^T lanes are head dims
 #pragma unroll
       for (int r = 0; r < NQ; ++r) {
@@ -665,19 +586,6 @@ __global__ void __launch_bounds__(um::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
 }
 
 // A cache [rows][512 dims] as a 2-D bf16 tensor with 128-byte swizzled boxes
