@@ -268,10 +268,15 @@ __global__ void __launch_bounds__(WPI > 8 ? WPI * 32 : 256, WPI > 16 ? 2 : WPI >
 // of refs: one launch of one block, or, above kOneBlockPages pages, of a
 // cluster of 8, each block a consecutive range of the pages, the ranges' totals
 // exchanged through distributed shared memory (16 sequences, 1100 pages:
-// 13.3 us in a cluster that kept its lists in global memory).
+// 13.3 us in a cluster that kept its lists in global memory). Measured with the
+// free pages at the high end (reserve, 64 sequences) or anywhere (compact), one
+// block / cluster: 1000 pages 4.3 / 6.6 and 2.9 / 5.3 us, 4096 pages 6.0 / 6.8
+// and 5.1 / 6.3, 8192 pages 7.8 / 6.8 and 7.7 / 6.1, 16384 pages 11.5 / 7.2 and
+// 13.6 / 7.2; 131072 pages in a cluster 15.6 and 18.4. A turn of 1024 pages a
+// block, its load, scan and two barriers, is what they take.
 constexpr int kCluster = 8;
 constexpr int kBookThreads = 1024;
-constexpr int kOneBlockPages = 16384;
+constexpr int kOneBlockPages = 6144;
 constexpr int kSharedSeqs = 1024;  // sequences whose lists stay in shared memory
 
 __device__ __forceinline__ int page_free(int refs) { return refs <= 0 ? 1 : 0; }
