@@ -172,9 +172,10 @@ size_t fd_pages_workspace_bytes(int B, int num_pages);
 
 /*
  * A list of moves: int32 [2 * (room + 1)]. moves[0] is the number of moves n,
- * moves[1] the number of free pages that are left, moves[2 + 2 i] and
- * moves[3 + 2 i] the source and the destination of move i < n; entries behind
- * them are left as they were.
+ * moves[1] the number of free pages that were not handed out (a page that this
+ * call of fd_pages_reserve took from its last owner is free beside them),
+ * moves[2 + 2 i] and moves[3 + 2 i] the source and the destination of move
+ * i < n; entries behind them are left as they were.
  *
  * fd_pages_reserve: room for grow[b] more tokens (int32 [B]; NULL: one for
  * each; <= 0: none) of every sequence. A sequence needs a page for each

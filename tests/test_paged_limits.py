@@ -162,3 +162,17 @@ def test_threads_on_their_default_streams_have_a_workspace_each():
     assert not failed
     assert free[0] - free[1] >= 9 << 20 and free[1] - free[2] >= 9 << 20
     assert all(torch.equal(out.view(torch.int16), want.view(torch.int16)) for out in outs)
+
+
+@pytest.mark.gpu
+def test_reserve_counts_free_pages_that_were_not_handed_out():
+    """Two owners of one begun page, and both write: each gets a copy, the original is free, and moves[1] does not count it."""
+    dev = empty(1, 3, 8, 16)
+    dev.reserve([5])
+    dev.fork([0, 0])
+    _, moves = dev.reserve([1, 1])
+    assert moves == [(0, 1), (0, 2)] and dev.book.refs.tolist() == [0, 1, 1, 0, 0, 0, 0, 0]
+    refs = dev.refs.clone()
+    fd.fd_pages_reserve(dev.table, dev.lens, dev.refs, torch.zeros(2, dtype=torch.int32, device=DEV),
+                        torch.empty(2, dtype=torch.int32, device=DEV), dev.moves, *dev.ws(), 2, 3, 8, 16)
+    assert dev.moves[:2].tolist() == [0, 6] and torch.equal(dev.refs, refs)  # the next call does
