@@ -418,7 +418,9 @@ struct Cut {
 // less and take the lower one (a move at 2^3 / 2^4 / 2^5: ragged batch E4M3 107 / 106 / 105 us, 4 x 131072 MQA 97.7 /
 // 97.6 / 97.6, both before the issue loops were rolled).
 constexpr float kTop8 = 7.f, kLazy8 = 5.f, kLazy8Shared = 3.f;
-constexpr float kLazy16 = 8.f, kBias16 = 0.f;
+// bf16: 2^(s - m) is at most 2^8, and enters the product with V times 2^-8: no value that is finite in V leaves fp32
+// where the largest weight meets it.
+constexpr float kLazy16 = 8.f, kBias16 = 0.f, kUnit16 = 0x1p-8f;
 
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ Maps maps, const PagedArgs a) {
@@ -1048,13 +1050,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           tmem_st_wait();
         }
       }
-      const float vs = C::KV8 ? ksvs.y * vunit[0] * vunit[1] : 1.f;
+      const float vs = C::KV8 ? ksvs.y * vunit[0] * vunit[1] : kUnit16;
       float w[C::NQ];
 #pragma unroll
       for (int r = 0; r < C::NQ; ++r) {
         w[r] = exp2f(sc[r] - ref[r]);
         l_part[r] += w[r];
-        if constexpr (C::KV8) w[r] *= vs;
+        w[r] *= vs;
       }
 
       // P(i) -> the group's buffer; its last reader, P.V(i - 2), must be done
@@ -1149,8 +1151,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             fac[C::NQ + tq] = e1 * by * pow2_of((grp == 1 ? vref : v_other) - low);
             if (tq == 0) vrefs[2 + grp] = low;
           } else {
-            fac[tq] = e0 * by;
-            fac[C::NQ + tq] = e1 * by;
+            fac[tq] = e0 * by * (1.f / kUnit16);
+            fac[C::NQ + tq] = e1 * by * (1.f / kUnit16);
           }
           if (!direct && tq < G && (!both || grp == 0))
             reinterpret_cast<float2*>(a.ws_ml)[static_cast<size_t>(slot) * G + tq] = make_float2(m, l);
@@ -1253,7 +1255,6 @@ constexpr int kMergeThreads = 256;
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedArgs a) {
   __shared__ float4 acc[kMergeThreads];
   extern __shared__ float factor[];  // [rows of this block][parts]
-  __shared__ float inv[16];
   grid_dependency_wait();
   grid_launch_dependents();
   const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1298,18 +1299,24 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
         }
         for (int p = lane + 32 * kHeld; p < parts; p += 32) m = fmaxf(m, ml[static_cast<size_t>(slot_of(p)) * G + q].x);
         for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+        // each part's share of all weights: the output is the mean of the parts' means, with these factors
         float l = 0.f;
-        auto one = [&](int p, const float2& v) {
-          const float f = exp2f(v.x - m) * v.y;
-          factor[(q - r0) * parts + p] = f;
-          l += f;
+        auto weight = [&](int p) {
+          const float2 v = ml[static_cast<size_t>(slot_of(p)) * G + q];
+          return exp2f(v.x - m) * v.y;
         };
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j)
-          if (lane + 32 * j < parts) one(lane + 32 * j, y[j]);
-        for (int p = lane + 32 * kHeld; p < parts; p += 32) one(p, ml[static_cast<size_t>(slot_of(p)) * G + q]);
+        for (int j = 0; j < kHeld; ++j) {
+          y[j].y *= exp2f(y[j].x - m);
+          l += y[j].y;
+        }
+        for (int p = lane + 32 * kHeld; p < parts; p += 32) l += weight(p);
         for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
-        if (lane == 0) inv[q] = l == 0.f ? 0.f : 1.f / l;
+        const float by = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+          if (lane + 32 * j < parts) factor[(q - r0) * parts + lane + 32 * j] = y[j].y * by;
+        for (int p = lane + 32 * kHeld; p < parts; p += 32) factor[(q - r0) * parts + p] = weight(p) * by;
       }
       __syncthreads();
     }
@@ -1334,13 +1341,11 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     if (g == 0) {
 #pragma unroll 4
       for (int j = 1; j < min(groups, parts); ++j) add(acc[j * n + tid], 1.f);
-      const float by = inv[r];
-      const float4 y = make_float4(s.x * by, s.y * by, s.z * by, s.w * by);
       const size_t at = (static_cast<size_t>(cut.b) * a.NH + static_cast<size_t>(cut.kvh) * G + r) * a.HS + 4 * d;
-      const uint32_t lo = f32_to_bf16_bits(y.x) | (static_cast<uint32_t>(f32_to_bf16_bits(y.y)) << 16);
-      const uint32_t hi = f32_to_bf16_bits(y.z) | (static_cast<uint32_t>(f32_to_bf16_bits(y.w)) << 16);
+      const uint32_t lo = f32_to_bf16_bits(s.x) | (static_cast<uint32_t>(f32_to_bf16_bits(s.y)) << 16);
+      const uint32_t hi = f32_to_bf16_bits(s.z) | (static_cast<uint32_t>(f32_to_bf16_bits(s.w)) << 16);
       *reinterpret_cast<uint2*>(a.out + at) = make_uint2(lo, hi);
-      if (a.out_f32) *reinterpret_cast<float4*>(a.out_f32 + at) = y;
+      if (a.out_f32) *reinterpret_cast<float4*>(a.out_f32 + at) = s;
     }
     __syncthreads();
   }

@@ -108,7 +108,8 @@ int fd_paged_plan_sms(int B, int NH, int NKV, int HS, int page_size, int max_pag
  * 2^-30 of that, so n positions of weights that are that small may add n times
  * as much to the error); products accumulate in fp32. Every scale that is not
  * negative is taken, 0 and subnormals too. bf16: q enters as it
- * is, the weights as three bf16 terms (2^-24).
+ * is, the weights, at most 1, as three bf16 terms (2^-24); like the products of
+ * any softmax in fp32, theirs with V overflow where they add up to 2^128.
  * fd_paged_attn makes its plan for the current device and uses a workspace
  * the library owns, one per (device, stream; the per-thread default stream is a
  * stream of its own in each thread): the first call for a pair

@@ -132,14 +132,40 @@ def test_small_elements_of_q_beside_a_large_one(kv, HS, G):
     assert off <= rel, f"2^{math.log2(off):.1f} against 2^{math.log2(rel):.1f}"
 
 
+@pytest.mark.parametrize("HS,G", [(64, 4), (128, 8), (512, 16)])
+@pytest.mark.parametrize("n,at", [(300, 280), (9000, 8990)])
+def test_largest_values_behind_a_lagging_reference(HS, G, n, at):
+    """bf16: a value of the type's largest size at a position whose score lies 7.2 powers of two above those of the group's tiles
+    before it, too few to move the reference; the other values are 0. The output is its part of the softmax, which is finite.
+    320 sequences of the same pages, so that most bands lie in one share.
+    Bound: that of test_weights_hold_24_bits, for a score of 7.2 instead of 2, and the sum of n weights."""
+    P, B = 16, 320
+    N = -(-n // P)
+    k, v = torch.zeros(N, 1, P, HS), torch.zeros(N, 1, P, HS)
+    top = torch.finfo(torch.bfloat16).max
+    k[at // P, 0, at % P, 0], v[at // P, 0, at % P] = 5.0, top
+    q = torch.zeros(B, G, HS)
+    q[:, :, 0] = 1
+    out16, out32, err = run_attn(BF16, q.bfloat16(), k.bfloat16(), None, v.bfloat16(), None,
+                                 np.tile(np.arange(N, dtype=np.int32), (B, 1)), [n] * B, 0, 1.0)
+    assert err == 0
+    want = math.exp(5) / (math.exp(5) + n - 1) * float(torch.tensor(top).bfloat16())
+    off = (out32.double() / want - 1).abs().max().item()
+    assert off <= 2.0 ** -17 + (n / 128 + 64) * 2.0 ** -24, f"{off}"
+    assert torch.isfinite(out16).all()
+
+
 def check(kv, q, k, ks, v, vs, table, lens, out16, out32, e2):
     """Against the 64-bit reference; e2 bounds what the weights and the sums lose, relative to the largest value of the row.
-    Outputs below 2^-126 are multiples of fp32's least value: its half, 2^-150, is added, and bf16's, 2^-134."""
+    Below 2^-126 fp32 and bf16 round to multiples of their least values, by at most 2^-150 and 2^-134: fp32 once where a share's
+    mean is made and twice for each share that is merged (the product with its factor is added to a sum, sums are added), and a
+    share has 64 KB of K and V at least."""
     HS = q.shape[2]
     kr, vr = (k.double().numpy(), v.double().numpy()) if kv == BF16 else (k.numpy(), v.numpy())
     want, big, mass = ref.attend(q.double().numpy(), kr, vr, None if ks is None else ks.numpy(),
                                  None if vs is None else vs.numpy(), table, lens, 0, HS ** -0.5, k.shape[0])
-    lim = ((4 * HS * 2.0 ** -23 * mass + e2 + 2.0 ** -20) * big)[..., None] + 2.0 ** -150
+    shares = max(lens) * HS * (2 if kv == BF16 else 1) // 32768 + 2
+    lim = ((4 * HS * 2.0 ** -23 * mass + e2 + 2.0 ** -20) * big)[..., None] + (1 + 2 * shares) * 2.0 ** -150
     got = out32.double().numpy()
     assert np.isfinite(got).all(), f"{(~np.isfinite(got)).sum()} of {got.size} are not finite"
     err = np.abs(got - want)
