@@ -128,6 +128,16 @@ __device__ __forceinline__ uint2 quantise8(const uint4& v, float inv) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// y is a result rounded to the nearest float, err (its sign, at least) what it
+// lacks: the float towards zero of the exact result, with an odd last place if
+// that was not exact. E4M3 codes of it are the nearest of the exact result, which
+// those of y are not where y was rounded onto the middle of two codes.
+__device__ __forceinline__ float sticky(float y, float err) {
+  uint32_t u = __float_as_uint(y);
+  if (err != 0.f) u = (u - ((__float_as_uint(err) ^ u) >> 31)) | 1u;
+  return __uint_as_float(u);
+}
+
 // The same for any scale and any values: NaN where x is not finite, 0 where
 // s is 0. Out of line: the divisions' code would crowd the rest out of the
 // instruction cache.
@@ -138,7 +148,16 @@ __device__ __noinline__ uint2 quantise8_any(uint4 v, float s) {
   for (int i = 0; i < 4; ++i) {
     float x[2] = {__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u)};
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k) x[k] = isfinite(x[k]) ? (s > 0.f ? x[k] / s : 0.f) : __int_as_float(0x7fffffff);
+    for (int k = 0; k < 2; ++k) {
+      if (!isfinite(x[k])) {
+        x[k] = __int_as_float(0x7fffffff);
+      } else if (s > 0.f) {
+        const float y = x[k] / s;
+        x[k] = sticky(y, fmaf(-y, s, x[k]));
+      } else {
+        x[k] = 0.f;
+      }
+    }
     c[i] = quantise2(x[0], x[1]);
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
@@ -154,7 +173,8 @@ __device__ __forceinline__ float pow2_reciprocal(float s) {
 __device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
   const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(c & 0xffff), __NV_E4M3)));
   const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(c >> 16), __NV_E4M3)));
-  return quantise2(a.x * ratio, a.y * ratio) | (static_cast<uint32_t>(quantise2(b.x * ratio, b.y * ratio)) << 16);
+  auto by = [&](float x) { return sticky(x * ratio, fmaf(x, ratio, -(x * ratio))); };
+  return quantise2(by(a.x), by(a.y)) | (static_cast<uint32_t>(quantise2(by(b.x), by(b.y))) << 16);
 }
 
 // The largest of an item's values (WPI warps; all warps of the block call it).

@@ -1,4 +1,5 @@
-"""The paged cache at the ends of its ranges: many heads, many sequences, the largest batches of positions, several threads."""
+"""The paged cache at the ends of its ranges: many heads, many sequences, the largest batches of positions, several threads, codes next
+to ties."""
 
 import threading
 
@@ -7,6 +8,7 @@ import pytest
 import torch
 
 import decode_attention_04_gb300 as fd
+import paged_ref as ref
 from test_paged_gpu import case, empty
 
 BF16, E4M3 = fd.FD_KV_BF16, fd.FD_KV_E4M3
@@ -176,3 +178,70 @@ def test_reserve_counts_free_pages_that_were_not_handed_out():
     fd.fd_pages_reserve(dev.table, dev.lens, dev.refs, torch.zeros(2, dtype=torch.int32, device=DEV),
                         torch.empty(2, dtype=torch.int32, device=DEV), dev.moves, *dev.ws(), 2, 3, 8, 16)
     assert dev.moves[:2].tolist() == [0, 6] and torch.equal(dev.refs, refs)  # the next call does
+
+
+def _near_ties():
+    """(x, s): bf16 values and fp32 scales whose quotient is within 2^-24 of the middle of two codes, but not on it."""
+    out = []
+    for middle in range(17, 33, 2):
+        for x in range(128, 256):
+            s = np.float32(x / middle)
+            if float(s) * middle != x:
+                out.append((float(x), float(s)))
+    return out
+
+
+@pytest.mark.gpu
+def test_append_codes_next_to_the_middle_of_two():
+    """Scales that are no powers of two, as a cache from elsewhere has them: x / scale next to a tie goes to the nearer code, not
+    to the one that a quotient rounded onto the tie gives."""
+    cases = _near_ties()
+    assert len(cases) > 500
+    HS, P, NKV = 64, 16, len(cases)  # a head for each case, as each has a scale
+    x = torch.tensor([c[0] for c in cases], dtype=torch.float64)
+    s = torch.tensor([c[1] for c in cases], dtype=torch.float64)
+    sign = torch.where(torch.arange(HS) % 2 == 0, 1.0, -1.0)
+    new = (x[:, None] * sign)[None].bfloat16()
+    assert torch.equal(new.double()[0, :, 0], x)
+    codes = torch.full((1, NKV, P, HS), 0x38, dtype=torch.uint8)  # earlier tokens: ones
+    want = ref.e4m3_code((new[0].double() / s[:, None]).numpy())
+    pools, scales = [codes.to(DEV) for _ in range(2)], [s.float()[None].to(DEV) for _ in range(2)]
+    rows = torch.stack([new, new], 1).to(DEV)
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.full((1,), 2, dtype=torch.int32, device=DEV)
+    fd.fd_paged_append(rows, rows[:, 1], *pools, *scales, table, lens, None, None, 1, 1, NKV, HS, P, 1, 1, rows.stride(0),
+                       rows.stride(0), E4M3)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(scales[i].cpu()[0], s.float())  # no scale rose
+        got = pools[i][0, :, 1].cpu().numpy()
+        assert np.array_equal(got, want), f"{(got != want).sum()} of {got.size} codes differ"
+
+
+@pytest.mark.gpu
+def test_append_rounds_earlier_codes_next_to_the_middle_of_two():
+    """Codes whose product with old scale / new scale is next to a tie, where a new token raises a scale that is no power of two."""
+    HS, P = 64, 16
+    held = [c for c in range(9, 0x78) if c & 7 in (3, 5, 7)]  # codes of odd significands 11, 13, 15
+    pairs = []
+    for c in held:
+        for middle in range(17, 33, 2):
+            old = np.float32(middle / (8 + (c & 7)) / 4)
+            if float(old) * (8 + (c & 7)) * 4 != middle and 0.25 < old < 0.9:
+                pairs.append((c, float(old)))
+    NKV = len(pairs)
+    assert NKV > 300
+    old = torch.tensor([p[1] for p in pairs], dtype=torch.float64)
+    codes = torch.zeros(1, NKV, P, HS, dtype=torch.uint8)
+    codes[0, :, 0] = torch.tensor([p[0] for p in pairs], dtype=torch.uint8)[:, None]
+    codes[0, :, 0, 1::2] |= 0x80
+    want = ref.e4m3_code(ref.TABLE[codes[0, :, 0].numpy()] * old[:, None].numpy())
+    pools, scales = [codes.to(DEV) for _ in range(2)], [old.float()[None].to(DEV) for _ in range(2)]
+    rows = torch.full((1, 2, NKV, HS), 448.0, device=DEV).bfloat16()  # the new scale is 1
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.full((1,), 2, dtype=torch.int32, device=DEV)
+    fd.fd_paged_append(rows, rows[:, 1], *pools, *scales, table, lens, None, None, 1, 1, NKV, HS, P, 1, 1, rows.stride(0),
+                       rows.stride(0), E4M3)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert (scales[i] == 1).all()
+        got = pools[i][0, :, 0].cpu().numpy()
+        assert np.array_equal(got, want), f"{(got != want).sum()} of {got.size} codes differ"
