@@ -7,11 +7,10 @@ A = scale * sum_d |q_d k_d| of a score and n the products summed in fp32:
     each addition off by at most 2^-23 of the partial sums' bound, which also holds
     where the adder truncates), and a weight by twice that, relatively, as its
     softmax's sum is off as well: e1 = 2 * 2 * HS * 2^-23 * A;
-  * E4M3: q enters as two E4M3 terms that leave at most 2^-15 of the row's largest element
-    (2^-10 of 1 where that element is at most 2^5 in units of the split's step), which for the
-    test's values (elements above 2^-14 of the largest are exact) is inside e1;
-    a weight as three terms: 2^-12 of itself or 2^-19 of the largest: e2 = 2^-11;
-    bf16: two terms, 2^-17: e2 = 2^-16;
+  * E4M3: q enters as E4M3 terms that leave at most 2^-21 of the row's largest element, which for
+    the test's values (elements above 2^-13 of the largest are exact) is inside e1;
+    a weight leaves at most 2^-24 of itself or 2^-30 of the largest: e2 = 2^-11 is wide for any n below 2^18;
+    bf16: 2^-24, and e2 = 2^-16 is wide as well (test_paged_values_gpu.py has the close bounds);
   * the output is a mean of values of at most |V|: |error| <= (e1 + e2 + 2^-20) |V|;
   * the bf16 output adds half a step, 2^-8 of the value.
 """
