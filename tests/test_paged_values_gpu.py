@@ -155,7 +155,7 @@ def test_largest_values_behind_a_lagging_reference(HS, G, n, at):
     assert torch.isfinite(out16).all()
 
 
-def check(kv, q, k, ks, v, vs, table, lens, out16, out32, e2):
+def check(kv, q, k, ks, v, vs, table, lens, out16, out32, e2, window=0):
     """Against the 64-bit reference; e2 bounds what the weights and the sums lose, relative to the largest value of the row.
     Below 2^-126 fp32 and bf16 round to multiples of their least values, by at most 2^-150 and 2^-134: fp32 once where a share's
     mean is made and twice for each share that is merged (the product with its factor is added to a sum, sums are added), and a
@@ -163,7 +163,7 @@ def check(kv, q, k, ks, v, vs, table, lens, out16, out32, e2):
     HS = q.shape[2]
     kr, vr = (k.double().numpy(), v.double().numpy()) if kv == BF16 else (k.numpy(), v.numpy())
     want, big, mass = ref.attend(q.double().numpy(), kr, vr, None if ks is None else ks.numpy(),
-                                 None if vs is None else vs.numpy(), table, lens, 0, HS ** -0.5, k.shape[0])
+                                 None if vs is None else vs.numpy(), table, lens, window, HS ** -0.5, k.shape[0])
     shares = max(lens) * HS * (2 if kv == BF16 else 1) // 32768 + 2
     lim = ((4 * HS * 2.0 ** -23 * mass + e2 + 2.0 ** -20) * big)[..., None] + (1 + 2 * shares) * 2.0 ** -150
     got = out32.double().numpy()
@@ -277,3 +277,22 @@ def test_zeros_that_the_writer_stored():
     out16, out32, err = run_attn(E4M3, q, k, ks, v, vs, table, [n], 0)
     assert err == 0
     check(E4M3, q, k, ks, v, vs, table, [n], out16, out32, lost(n))
+
+
+@pytest.mark.parametrize("HS,G,NKV,P,window", [(64, 4, 3, 16, 0), (128, 8, 2, 32, 0), (256, 16, 1, 16, 100), (512, 16, 2, 16, 0)])
+def test_far_scales_in_many_short_bands(HS, G, NKV, P, window):
+    """A batch of short sequences, several bands to a block, whose blocks have scales of their own: a third zero, the others
+    from 2^-126 to 2^100. A band's scales have no effect on the next one's."""
+    rng = np.random.default_rng(HS)
+    lens = [int(x) for x in rng.integers(0, 330, 60)] + [0, 1, P]
+    wide = 330 // P + 1
+    N = sum(-(-n // P) for n in lens) + 1
+    k, ks, _ = make_pool(E4M3, N, NKV, P, HS, 3)
+    v, _, _ = make_pool(E4M3, N, NKV, P, HS, 4)
+    table = make_table(lens, P, wide, N, 5)
+    e = rng.integers(-126, 101, (N, NKV))
+    vs = torch.from_numpy(np.where(rng.random((N, NKV)) < 1 / 3, 0.0, np.exp2(e.astype(np.float64)))).float()
+    q = _values((len(lens), NKV * G, HS), 7).bfloat16()
+    out16, out32, err = run_attn(E4M3, q, k, ks, v, vs, table, lens, window)
+    assert err == 0
+    check(E4M3, q, k, ks, v, vs, table, lens, out16, out32, lost(330), window)
